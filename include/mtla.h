@@ -406,6 +406,153 @@ mtla_status mtla_train_merge_bwd(const mtla_dims *dims, int32_t B, int32_t T, co
                                  float *dW_c, float *db_c, float *dP, void *workspace, size_t workspace_bytes,
                                  int32_t *dev_err, void *stream);
 
+/*
+ * Paged serving: chunks of new tokens over a paged cache ([merge], [mask],
+ * [rope], [fig2](a)).
+ *
+ * A paged cache is a pool of pages of page_rows cache rows each; sequence b's
+ * row j (0-based) is row j mod page_rows of page
+ * block_table[b * table_pages + j / page_rows].  Pages may be shared by
+ * sequences that only read them; a page that a call writes belongs to one
+ * sequence.
+ *   page_rows: a multiple of 8 (16 and 64 are usual); row_stride >= r + d_R
+ *   elements, a multiple of 16 bytes; num_pages * page_rows < 2^31.
+ *   A table entry outside [0, num_pages) that a call needs sets
+ *   MTLA_DEVERR_CAPACITY; rows of such a page are not written, and read as
+ *   zeros.
+ */
+typedef struct {
+  void *pages;                /* [num_pages, page_rows, row_stride] cache dtype */
+  int64_t num_pages;
+  int64_t row_stride;         /* elements between rows                          */
+  int32_t page_rows;
+  int32_t table_pages;        /* entries of one sequence's table                */
+  const int32_t *block_table; /* [B, table_pages]                               */
+} mtla_paged_cache;
+
+/* The new tokens of B sequences, one after another in the token arrays of N
+ * rows: sequence b's are rows tok_start[b] .. tok_start[b+1] - 1 (any number,
+ * none included), at times t_prev[b] + 1, t_prev[b] + 2, ... (1-indexed).  With
+ * tok_count only the first tok_count[b] of them are taken.  tok_start ascends;
+ * rows that no sequence takes (behind the last one, or past tok_count) are
+ * neither read nor written. */
+typedef struct {
+  int32_t N;                  /* rows of the token arrays                       */
+  int32_t reserved;           /* 0                                              */
+  const int32_t *tok_start;   /* [B + 1]                                        */
+  const int32_t *tok_count;   /* [B] or NULL                                    */
+  const int32_t *t_prev;      /* [B] tokens processed before this chunk         */
+} mtla_chunk;
+
+/*
+ * mtla_paged_append — merge a chunk of new tokens of every sequence into the
+ * paged cache, with the RoPE rotation on the way.  Token i of sequence b, at
+ * time t = t_prev[b] + 1 + i and group j = ceil(t/s):
+ *   k^R  = kR_new rotated as position t - 1 (channel pair (2k, 2k+1) by
+ *          (t-1) rope_base^(-2k/d_R)); rope_base == 0 takes kR_new as rotated;
+ *   e    = sigmoid((c W_c + b_c) * P[j-1]) * [c ; k^R];
+ *   S_t  = e if t opens its group, else S_{t-1} + e,
+ * S kept in fp32 (S before the chunk is tail_in[b]) and rounded to the cache
+ * dtype only where it is stored:
+ *   row_state [N, D] cache dtype (nullable): S_t of every token, the row its
+ *             own query attends (mtla_paged_attn);
+ *   the cache row j - 1 of every group the chunk touches: S at the group's
+ *             last token of the chunk;
+ *   tail_out  [B, D] fp32: S at the chunk's last token (tail_in[b] for a
+ *             sequence without tokens);
+ *   t_out     [B] = t_prev + tokens taken; cache_len [B] (nullable) =
+ *             ceil(t_out / s).
+ *   merge: c_new [N, r], kR_new [N, d_R] (cache dtype); W_c, b_c, P, J_max.
+ *   q_rope    [N, H, d_R] (nullable): the chunk's RoPE queries, written rotated
+ *             (at the token's position, cache dtype) to q_rope_out, which may
+ *             be q_rope itself.
+ * Only t_out, tail_out, row_state, q_rope_out and cache rows are written, and
+ * no state that is read is overwritten: tail_out and t_out must not overlap
+ * tail_in and t_prev.  So a chunk can be appended again with another tok_count:
+ * after a verification, the call with tok_count = n_keep leaves the cache rows,
+ * the tail and the lengths that the kept tokens alone would have left (rows of
+ * later groups hold stale values until they are appended again).  How a
+ * sequence's tokens are cut into chunks does not change the sums: the open
+ * group's sum travels in fp32.
+ * A sequence whose chunk does not fit (ceil((t_prev + tokens)/s) above
+ * table_pages * page_rows: MTLA_DEVERR_CAPACITY, as for t_prev < 0; above
+ * J_max: MTLA_DEVERR_PE_RANGE) takes none of its tokens.
+ *   workspace: mtla_paged_workspace_bytes(dims, B, N, MTLA_PAGED_APPEND) (0
+ *   bytes today; NULL is fine then).
+ * d_R even where anything is rotated (MTLA_ERR_UNSUPPORTED otherwise).
+ */
+mtla_status mtla_paged_append(const mtla_dims *dims, int32_t B, const mtla_chunk *chunk,
+                              const mtla_merge_args *merge, double rope_base,
+                              const void *q_rope, void *q_rope_out,
+                              const mtla_paged_cache *cache, const float *tail_in, float *tail_out,
+                              int32_t *t_out, int32_t *cache_len, void *row_state,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/*
+ * mtla_paged_attn — attention of a chunk of new tokens over the paged cache
+ * ([mask], [rope], [fig2](c)): the query of token i of sequence b, at time t,
+ * attends the complete groups before its own (cache rows 0 .. ceil(t/s) - 2)
+ * and its own state row_state[token]; per head
+ *   score_n = (q_abs . c_hat_n + q_rope . k_hat^R_n) / sqrt(d_h),
+ *   out = sum_n softmax(score)_n c_hat_n,  lse = ln sum_n e^score_n.
+ * It reads the cache as mtla_paged_append of the same chunk left it.  One token
+ * a sequence is a decode step, several a speculative step, many a piece of a
+ * prompt.
+ *   q_abs [N, H, r], q_rope [N, H, d_R] (RoPE applied), row_state [N, D]: cache
+ *   dtype; out [N, H, r] in out_dtype (the cache dtype, or MTLA_F32); lse
+ *   [N, H] fp32 (nullable).
+ * A sequence whose rows exceed its table (or with t_prev < 0) sets
+ * MTLA_DEVERR_CAPACITY and its rows of out and lse are left as they were.
+ *   workspace: mtla_paged_workspace_bytes(dims, B, N, MTLA_PAGED_ATTN) bytes; no
+ *   initialisation; for calls that run one after another.
+ */
+mtla_status mtla_paged_attn(const mtla_dims *dims, int32_t B, const mtla_chunk *chunk,
+                            const void *q_abs, const void *q_rope, const void *row_state,
+                            const mtla_paged_cache *cache, void *out, int32_t out_dtype, float *lse,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+#define MTLA_PAGED_APPEND 1
+#define MTLA_PAGED_ATTN 2
+
+/* Workspace bytes of mtla_paged_append / mtla_paged_attn for B sequences and
+ * token arrays of N rows (0 if none, or on unsupported arguments).  Queries the
+ * current device. */
+size_t mtla_paged_workspace_bytes(const mtla_dims *dims, int32_t B, int32_t N, int32_t which);
+
+/*
+ * mtla_verify_drafts — keep or drop drafted tokens by the target model's
+ * probabilities, from given random numbers (speculative sampling: the kept
+ * tokens and the next one follow the target's distribution).  Sequence b's
+ * chunk is rows tok_start[b] .. tok_start[b+1] - 1 of the token arrays: its
+ * first token is the last one already certain, the others are drafts.  For
+ * its rows i = 0, 1, ...:
+ *   p[i]  the target's probabilities of the token after token i;
+ *   q[i]  the probabilities that draft i + 1 was drawn from (the last row of a
+ *         chunk is not read); q == NULL: every draft was certain (a one-hot
+ *         q);
+ *   draft x = tokens[i + 1] is kept iff u_accept[i] q[i][x] < p[i][x] and all
+ *   drafts before it are kept.
+ *   n_keep[b]     = 1 + the number of kept drafts (0 for an empty chunk);
+ *   next_token[b] : drawn from max(p[i] - q[i], 0) of the row i whose draft was
+ *   dropped, or from p of the last row when every draft was kept (or from
+ *   p[i] where the difference is zero everywhere), as the lowest index whose
+ *   running sum of weights exceeds u_sample[b] times their sum.  Products,
+ *   differences and sums are taken in double precision.  -1 for an empty
+ *   chunk, and with MTLA_DEVERR_EMPTY where p has no positive entry.
+ *   p [N, V] fp32, rows ld_p >= V elements apart, q likewise with ld_q; entries
+ *   that are NaN, infinite or below zero count as zero; rows need not sum to
+ *   one.  tokens [N] int32 (a draft outside [0, V) is dropped and sets
+ *   MTLA_DEVERR_TOKEN), tok_start [B + 1] int32, u_accept [N] and u_sample [B]
+ *   fp32 in [0, 1); n_keep, next_token [B] int32, written.
+ *   1 <= V <= 2^24.  4-byte alignment is enough for every array.
+ */
+#define MTLA_DEVERR_TOKEN 16 /* a token index outside the vocabulary */
+
+mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float *p, int64_t ld_p, const float *q,
+                               int64_t ld_q, const int32_t *tokens, const int32_t *tok_start,
+                               const float *u_accept, const float *u_sample, int32_t *n_keep,
+                               int32_t *next_token, int32_t *dev_err, void *stream);
+
 #define MTLA_WS_DECODE 0
 #define MTLA_PROJ_IN 1
 #define MTLA_PROJ_OUT 2

@@ -27,7 +27,8 @@ PROJ_IN, PROJ_OUT = 1, 2
 TRAIN_ATTN_BWD, TRAIN_KV_BWD, TRAIN_MERGE_BWD = 1, 2, 3  # MTLA_TRAIN_*
 DECODE_STATIC_SCRATCH_BYTES = 24 << 20  # MTLA_DECODE_STATIC_SCRATCH_BYTES
 MAX_NEW_TOKENS = 16  # MTLA_MAX_NEW_TOKENS
-DEVERR_PE_RANGE, DEVERR_CAPACITY, DEVERR_EMPTY, DEVERR_TIMEOUT = 1, 2, 4, 8
+PAGED_APPEND, PAGED_ATTN = 1, 2  # MTLA_PAGED_*
+DEVERR_PE_RANGE, DEVERR_CAPACITY, DEVERR_EMPTY, DEVERR_TIMEOUT, DEVERR_TOKEN = 1, 2, 4, 8, 16
 _c = ctypes
 
 
@@ -39,6 +40,16 @@ class _Dims(_c.Structure):
 class _Merge(_c.Structure):
     _fields_ = [("c_new", _c.c_void_p), ("kR_new", _c.c_void_p), ("W_c", _c.c_void_p), ("b_c", _c.c_void_p),
                 ("P", _c.c_void_p), ("J_max", _c.c_int32)]
+
+
+class _Paged(_c.Structure):
+    _fields_ = [("pages", _c.c_void_p), ("num_pages", _c.c_int64), ("row_stride", _c.c_int64),
+                ("page_rows", _c.c_int32), ("table_pages", _c.c_int32), ("block_table", _c.c_void_p)]
+
+
+class _Chunk(_c.Structure):
+    _fields_ = [("N", _c.c_int32), ("reserved", _c.c_int32), ("tok_start", _c.c_void_p), ("tok_count", _c.c_void_p),
+                ("t_prev", _c.c_void_p)]
 
 
 _P = _c.c_void_p
@@ -90,6 +101,17 @@ lib.mtla_train_merge_bwd.restype = _c.c_int
 lib.mtla_train_merge_bwd.argtypes = [_DIMS_P, _I32, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P,
                                      _P]
 
+lib.mtla_paged_workspace_bytes.restype = _SZ
+lib.mtla_paged_workspace_bytes.argtypes = [_DIMS_P, _I32, _I32, _I32]
+lib.mtla_paged_append.restype = _c.c_int
+lib.mtla_paged_append.argtypes = [_DIMS_P, _I32, _c.POINTER(_Chunk), _MERGE_P, _c.c_double, _P, _P,
+                                  _c.POINTER(_Paged)] + [_P] * 6 + [_SZ, _P, _P]
+lib.mtla_paged_attn.restype = _c.c_int
+lib.mtla_paged_attn.argtypes = [_DIMS_P, _I32, _c.POINTER(_Chunk), _P, _P, _P, _c.POINTER(_Paged), _P, _I32, _P, _P,
+                                _SZ, _P, _P]
+lib.mtla_verify_drafts.restype = _c.c_int
+lib.mtla_verify_drafts.argtypes = [_I32, _I32, _I32, _P, _I64, _P, _I64] + [_P] * 8
+
 
 class MtlaError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -137,6 +159,27 @@ def _merge(m):
             _MERGE_CACHE.clear()
         st = _MERGE_CACHE[key] = _Merge(*key)
     return _c.byref(st)
+
+
+def merge_args(c_new, kR_new, W_c, b_c, P, J_max) -> _Merge:
+    """mtla_merge_args of these tensors, for the paged calls; keeps them alive."""
+    m = _Merge(_ptr(c_new), _ptr(kR_new), _ptr(W_c), _ptr(b_c), _ptr(P), J_max)
+    m._keep = (c_new, kR_new, W_c, b_c, P)
+    return m
+
+
+def chunk(N, tok_start, t_prev, tok_count=None) -> _Chunk:
+    """mtla_chunk: the new tokens of a batch; keeps its tensors alive."""
+    c = _Chunk(N, 0, _ptr(tok_start), _ptr(tok_count), _ptr(t_prev))
+    c._keep = (tok_start, tok_count, t_prev)
+    return c
+
+
+def paged_cache(pages, num_pages, page_rows, row_stride, block_table, table_pages) -> _Paged:
+    """mtla_paged_cache: a pool of pages and the sequences' block tables; keeps its tensors alive."""
+    c = _Paged(_ptr(pages), num_pages, row_stride, page_rows, table_pages, _ptr(block_table))
+    c._keep = (pages, block_table)
+    return c
 
 
 def _check(status: int, where: str):
@@ -240,6 +283,32 @@ def mtla_project_out(d, B, dm, o, W_out, y, workspace, workspace_bytes, dev_err,
 
 def mtla_project_workspace_bytes(d, B, dm, which) -> int:
     return int(lib.mtla_project_workspace_bytes(_c.byref(d), B, dm, which))
+
+
+def mtla_paged_workspace_bytes(d, B, N, which) -> int:
+    return int(lib.mtla_paged_workspace_bytes(_c.byref(d), B, N, which))
+
+
+def mtla_paged_append(d, B, chunk, merge, rope_base, q_rope, q_rope_out, cache, tail_in, tail_out, t_out, cache_len,
+                      row_state, workspace, workspace_bytes, dev_err, stream=None):
+    _check(lib.mtla_paged_append(_c.byref(d), B, _c.byref(chunk), _c.byref(merge), rope_base, _ptr(q_rope),
+                                 _ptr(q_rope_out), _c.byref(cache), _ptr(tail_in), _ptr(tail_out), _ptr(t_out),
+                                 _ptr(cache_len), _ptr(row_state), _ptr(workspace), workspace_bytes, _ptr(dev_err),
+                                 _stream(stream)), "mtla_paged_append")
+
+
+def mtla_paged_attn(d, B, chunk, q_abs, q_rope, row_state, cache, out, out_dtype, lse, workspace, workspace_bytes,
+                    dev_err, stream=None):
+    _check(lib.mtla_paged_attn(_c.byref(d), B, _c.byref(chunk), _ptr(q_abs), _ptr(q_rope), _ptr(row_state),
+                               _c.byref(cache), _ptr(out), out_dtype, _ptr(lse), _ptr(workspace), workspace_bytes,
+                               _ptr(dev_err), _stream(stream)), "mtla_paged_attn")
+
+
+def mtla_verify_drafts(B, N, V, p, ld_p, q, ld_q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err,
+                       stream=None):
+    _check(lib.mtla_verify_drafts(B, N, V, _ptr(p), ld_p, _ptr(q), ld_q, _ptr(tokens), _ptr(tok_start),
+                                  _ptr(u_accept), _ptr(u_sample), _ptr(n_keep), _ptr(next_token), _ptr(dev_err),
+                                  _stream(stream)), "mtla_verify_drafts")
 
 
 def mtla_workspace_bytes(d, B, which=WS_DECODE) -> int:

@@ -203,6 +203,15 @@ bool encode_weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K) {
 
 }  // namespace
 
+namespace mtla {
+mtla_status check_call_dims(const mtla_dims* d) { return check_dims(d); }
+int current_device_sms() { return device_sms(); }
+bool encode_bf16_tiled_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  return encode_bf16_map(map, base, rank, dims, strides, box, swizzle);
+}
+}  // namespace mtla
+
 extern "C" {
 
 const char* mtla_status_string(mtla_status st) {

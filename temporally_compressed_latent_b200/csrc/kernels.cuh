@@ -5,6 +5,12 @@
 
 namespace mtla {
 
+// Host checks and tensor maps shared by the files of the C ABI (api.cu).
+mtla_status check_call_dims(const mtla_dims* d);
+int current_device_sms();  // 0 on error
+bool encode_bf16_tiled_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
+
 // Cache and per-sequence state (device pointers).
 struct SeqArgs {
   void* cache;

@@ -1,0 +1,439 @@
+// Chunks of new tokens over a paged cache: argument blocks, the token -> sequence
+// search, and the work partition of the attention kernels.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace mtla {
+
+struct ChunkDev {
+  int B, N;
+  const int32_t* tok_start;  // [B + 1]
+  const int32_t* tok_count;  // [B] or null
+  const int32_t* t_prev;     // [B]
+};
+struct PagesDev {
+  void* pages;
+  int64_t num_pages, row_stride;
+  const int32_t* table;      // [B, table_pages]
+  int page_rows, table_pages;
+};
+
+// A sequence's part of a chunk: token rows [first, first + n) at times t0 + 1 .. t0 + n.
+struct SeqWin {
+  int first, n;
+  int64_t t0;
+};
+// Read from the arrays with every value clamped into range, so that no index
+// formed from it leaves the token arrays whatever the arrays hold.
+__device__ __forceinline__ SeqWin seq_win(const ChunkDev& c, int b) {
+  SeqWin w;
+  const int s0 = c.tok_start[b], s1 = c.tok_start[b + 1];
+  w.first = s0 < 0 ? 0 : (s0 < c.N ? s0 : c.N);
+  const int end = s1 < w.first ? w.first : (s1 < c.N ? s1 : c.N);
+  w.n = end - w.first;
+  if (c.tok_count) {
+    const int k = c.tok_count[b];
+    if (k < w.n) w.n = k < 0 ? 0 : k;
+  }
+  w.t0 = c.t_prev[b];
+  return w;
+}
+__device__ __forceinline__ int64_t table_rows(const PagesDev& p) { return (int64_t)p.table_pages * p.page_rows; }
+
+// Pool row of sequence b's cache row g, or -1 (table entry outside the pool).  g < table_rows.
+__device__ __forceinline__ int64_t pool_row(const PagesDev& p, int b, int64_t g) {
+  const int64_t k = g / p.page_rows;
+  const int32_t page = p.table[(int64_t)b * p.table_pages + k];
+  return page >= 0 && page < p.num_pages ? (int64_t)page * p.page_rows + (g - k * p.page_rows) : -1;
+}
+
+// The sequence that owns token row i: the last b with tok_start[b] <= i, or -1.
+// Taken by a whole warp: every round narrows the range 32-fold (two dependent
+// loads for 1024 sequences; a binary search by one thread would take ten).
+__device__ __forceinline__ int warp_find_seq(const int32_t* tok_start, int B, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = -1, hi = B;  // the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo - 1 + 31) / 32;
+    const int at = lo + 1 + lane * step;
+    const bool below = at < hi && tok_start[at] <= i;
+    const int c = __popc(__ballot_sync(0xffffffffu, below));  // probes at or below i (a prefix, as tok_start ascends)
+    if (c > 0) lo = lo + 1 + (c - 1) * step;
+    else hi = lo + 1;
+    if (c > 0 && lo + step < hi) hi = lo + step;
+    // c == 0: nothing above lo qualifies
+  }
+  return lo;
+}
+
+// ----------------------------------------------------------------------------
+// RoPE angles: channel pair k turns by pos * base^(-2k/d_R).  The host passes
+// base^(-2k/d_R) / (2 pi), so the device needs one multiply in double, the
+// fraction of a turn (exact), and a single-precision sine and cosine of an
+// angle within half a turn: the angle of position 2^31 is as exact as that of
+// position 1 (absolute error near 2^-24 of a half turn).
+// ----------------------------------------------------------------------------
+constexpr int MAX_ROPE_PAIRS = 288;
+struct RopeTable {
+  double turns[MAX_ROPE_PAIRS];
+};
+__device__ __forceinline__ float2 rope_cos_sin(int64_t pos, double turns) {
+  const double a = (double)pos * turns;
+  const float f = (float)(a - rint(a));
+  float2 r;
+  sincospif(2.f * f, &r.y, &r.x);
+  return r;  // x = cos, y = sin
+}
+
+// ----------------------------------------------------------------------------
+// Work partition of the paged attention.
+//
+// An item is (sequence, up to tpt consecutive tokens of its chunk): all their
+// heads are the rows of one M tile.  Its columns, in order: the R = ceil(t/s) - 1
+// cache rows that its last token sees, padded to a multiple of 8, then the
+// tokens' own states (one virtual row a token), cut into key tiles of 8 q rows.
+// With kt key tiles an item weighs item_cost + kt.  The weights of all items,
+// one after another, form a line of length C that is cut into equal shares,
+// one a block: every block streams the same number of key tiles (to one),
+// whether the chunk is one token over a long cache (an item spans many
+// blocks) or a long prompt (a block takes many items).  Where a cut falls
+// inside an item its parts are combined by a second kernel.
+//
+// kt = ceil((8 ceil(R/8) + 8 g) / (8 q)) with g = ceil(tokens / 8); nested
+// floors of nested divisions fold into one,
+//   kt = floor((t + 7 s - 1 + 8 s (g + q - 1)) / (8 q s)),
+// linear in t, so the sum over a sequence's items is a sum of floors of a
+// linear function, which has a logarithmic-time form (floor_sum).
+// ----------------------------------------------------------------------------
+struct PlanArgs {
+  int s, tpt, q, item_cost;
+};
+// sum over i in [0, n) of floor((a i + b) / m), by the Euclidean recursion
+__device__ inline int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
+  uint64_t ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const uint64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint64_t x = m;
+    m = a;
+    a = x;
+  }
+  return (int64_t)ans;
+}
+// key tiles of an item whose last token has time t and which holds k tokens
+__device__ __forceinline__ int64_t item_tiles(const PlanArgs& a, int64_t t, int k) {
+  const int g = (k + 7) >> 3;
+  return (t + 7ll * a.s - 1 + 8ll * a.s * (g + a.q - 1)) / (8ll * a.q * a.s);
+}
+// weight of a sequence's first m items (chunk of n tokens after t0)
+__device__ inline int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int64_t m) {
+  const int64_t full = n / a.tpt, k = m < full ? m : full;
+  int64_t w = m * a.item_cost;
+  if (k == 1) w += item_tiles(a, t0 + a.tpt, a.tpt);
+  else if (k > 1)
+    w += floor_sum((uint64_t)k, 8ull * a.q * a.s, (uint64_t)a.tpt,
+                   (uint64_t)(t0 + a.tpt + 7ll * a.s - 1 + 8ll * a.s * (((a.tpt + 7) >> 3) + a.q - 1)));
+  if (m > full) w += item_tiles(a, t0 + n, n - (int)full * a.tpt);
+  return w;
+}
+
+// One item's part in a block.
+struct Item {
+  int b;            // sequence
+  int row0, ntok;   // token rows [row0, row0 + ntok)
+  int64_t t;        // time of the first of them
+  int64_t R;        // cache rows its last token sees
+  int kt0, kt1;     // key tiles of this part
+  int kt;           // key tiles of the item
+  int slot;         // partial-result slot, or -1: the whole item is here, its results go out directly
+};
+
+// Shares: block x of G takes [C x / G, C (x + 1) / G).
+__device__ __forceinline__ int64_t share_lo(int64_t C, int64_t G, int64_t x) { return C * x / G; }
+
+struct PlanShared {
+  int64_t warp_sum[32];
+  int64_t C, before;  // total weight; weight of the sequences before `b`
+  int b;              // sequence holding this block's first position
+};
+
+// The chunk window the attention takes (a sequence whose rows exceed its table,
+// or with a negative time, takes none).
+__device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p, int s, int b, int32_t* dev_err) {
+  SeqWin w = seq_win(c, b);
+  if (w.n > 0 && (w.t0 < 0 || group_of(w.t0 + w.n, s) - 1 > table_rows(p))) {
+    if (dev_err) set_err(dev_err, MTLA_DEVERR_CAPACITY);
+    w.n = 0;
+  }
+  return w;
+}
+
+// Taken by every thread of the block: the total weight C, and the sequence
+// that holds position share_lo(C, G, x).  One pass over the sequences (each
+// thread sums a run of them) and one block scan; the thread whose run holds
+// the position walks its run again.  x < 0: only C.
+template <int NT>
+__device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int grid, int x,
+                                  int32_t* dev_err, PlanShared* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (c.B + NT - 1) / NT;
+  const int b0 = tid * per < c.B ? tid * per : c.B, b1 = b0 + per < c.B ? b0 + per : c.B;
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqWin w = attn_win(c, p, a.s, b, x == 0 ? dev_err : nullptr);
+    sum += items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
+  }
+  int64_t pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) sh->warp_sum[warp] = pre;
+  if (tid == 0) sh->b = -1;
+  __syncthreads();
+  int64_t base = 0, C = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) base += sh->warp_sum[w];
+    C += sh->warp_sum[w];
+  }
+  if (tid == 0) sh->C = C;
+  const int64_t G = C < grid ? C : grid;
+  if (x >= 0 && x < G) {
+    const int64_t lo = share_lo(C, G, x);
+    int64_t at = base + pre - sum;
+    if (lo >= at && lo < at + sum) {
+      int b = b0;
+      for (; b + 1 < b1; ++b) {
+        const SeqWin w = attn_win(c, p, a.s, b, nullptr);
+        const int64_t k = items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
+        if (lo < at + k) break;
+        at += k;
+      }
+      sh->b = b;
+      sh->before = at;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks the items of block x's share in order.  Every lane of one warp calls
+// init and next together; results are warp-uniform.
+struct ItemWalk {
+  int64_t pos, hi, C, G;
+  int64_t start;          // position of the current item
+  int b, tile, x;
+  int batch;              // first sequence of the window batch in the lanes
+  int w_first, w_n;       // this lane's sequence batch + lane
+  int64_t w_t0;
+
+  __device__ __forceinline__ void load(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int b0) {
+    batch = b0;
+    const int bb = b0 + (threadIdx.x & 31);
+    SeqWin w;
+    w.first = 0;
+    w.n = 0;
+    w.t0 = 0;
+    if (bb < c.B) w = attn_win(c, p, a.s, bb, nullptr);
+    w_first = w.first;
+    w_n = w.n;
+    w_t0 = w.t0;
+  }
+
+  __device__ inline void init(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int grid, int x_,
+                              const PlanShared* sh) {
+    x = x_;
+    C = sh->C;
+    G = C < grid ? C : grid;
+    if (x >= G || sh->b < 0) {
+      pos = hi = 0;
+      return;
+    }
+    pos = share_lo(C, G, x);
+    hi = share_lo(C, G, x + 1);
+    b = sh->b;
+    load(c, p, a, b);
+    // the item of sequence b at offset pos - before: the largest tile whose
+    // earlier tiles weigh no more (32 candidates a round)
+    const int n = __shfl_sync(0xffffffffu, w_n, 0);
+    const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, 0), rem = pos - sh->before;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, up = (n + a.tpt - 1) / a.tpt;
+    while (up - lo > 1) {
+      const int step = (up - lo - 1 + 31) / 32, at = lo + 1 + lane * step;
+      const bool le = at < up && items_weight(a, t0, n, at) <= rem;
+      const int k = __popc(__ballot_sync(0xffffffffu, le));
+      if (k == 0) {
+        up = lo + 1;
+      } else {
+        lo = lo + 1 + (k - 1) * step;
+        if (lo + step < up) up = lo + step;
+      }
+    }
+    tile = lo;
+    start = sh->before + items_weight(a, t0, n, tile);
+  }
+
+  // The next item with key tiles in this share; false at the share's end.
+  __device__ inline bool next(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, Item* it) {
+    while (pos < hi) {
+      const int src = b - batch;
+      const int first = __shfl_sync(0xffffffffu, w_first, src), n = __shfl_sync(0xffffffffu, w_n, src);
+      const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, src);
+      const int i0 = tile * a.tpt, k = n - i0 < a.tpt ? n - i0 : a.tpt;
+      const int64_t kt = item_tiles(a, t0 + i0 + k, k), end = start + a.item_cost + kt;
+      const int64_t y = hi < end ? hi : end;
+      const int64_t k0 = pos - start - a.item_cost, k1 = y - start - a.item_cost;
+      it->b = b;
+      it->row0 = first + i0;
+      it->ntok = k;
+      it->t = t0 + i0 + 1;
+      it->R = group_of(t0 + i0 + k, a.s) - 1;
+      it->kt0 = k0 > 0 ? (int)k0 : 0;
+      it->kt1 = k1 > 0 ? (int)k1 : 0;
+      it->kt = (int)kt;
+      // outgoing parts (the item starts here and goes on) use slot 2 x + 1,
+      // the others 2 x: a block has at most one of each
+      it->slot = it->kt0 == 0 && it->kt1 == it->kt ? -1 : (it->kt0 == 0 ? 2 * x + 1 : 2 * x);
+      const bool some = it->kt1 > it->kt0;
+      item_start = start;
+      pos = y;
+      if (y == end) {  // on to the next item
+        start = end;
+        ++tile;
+        if (tile * a.tpt >= n) {
+          tile = 0;
+          ++b;
+          while (pos < hi) {  // the next sequence with tokens (one exists: positions are left)
+            if (b - batch >= 32) load(c, p, a, b);
+            const uint32_t has = __ballot_sync(0xffffffffu, w_n > 0) & (0xffffffffu << (b - batch));
+            if (has) {
+              b = batch + __ffs(has) - 1;
+              break;
+            }
+            b = batch + 32;
+            if (b >= c.B) {
+              pos = hi;
+              break;
+            }
+          }
+        }
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+  int64_t item_start;     // position of the item that next() returned
+};
+
+// What a block tells the combine kernel: the split item that ends in it.
+struct SplitDesc {
+  int row0, ntok;   // ntok == 0: none
+  int first;        // first block with a part of it
+  int pad;
+  int64_t C, G;
+};
+// The first block that holds a key tile of an item at position `start`: the
+// last x with share_lo(x) <= start + item_cost.
+__device__ __forceinline__ int first_block(const PlanArgs& a, int64_t C, int64_t G, int64_t start) {
+  return (int)(((start + a.item_cost + 1) * G - 1) / C);
+}
+
+// Partial results: slot (2 a block), row of the M tile: (max, sum) in log2
+// units and the unnormalised output, fp32.
+struct PartBuf {
+  SplitDesc* desc;  // [grid]
+  float2* ml;       // [2 grid][rows]
+  float* o;         // [2 grid][rows][r]
+};
+struct PagedLayout {
+  size_t desc, ml, o, total;
+};
+inline PagedLayout paged_layout(int grid, int rows, int r) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  PagedLayout l;
+  l.desc = 0;
+  l.ml = up((size_t)grid * sizeof(SplitDesc));
+  l.o = l.ml + up((size_t)2 * grid * rows * 8);
+  l.total = l.o + up((size_t)2 * grid * rows * r * 4);
+  return l;
+}
+
+struct PagedAttnArgs {
+  ChunkDev c;
+  PagesDev p;
+  PlanArgs plan;
+  PartBuf part;
+  const void *q_abs, *q_rope, *row_state;
+  void* out;
+  float* lse;
+  int32_t* dev_err;
+  int H, r, d_R;
+  int out_f32;
+  int rows;          // rows of an M tile (stride of the partial buffers)
+  float scale_log2;  // log2(e) / sqrt(d_h)
+};
+
+// generic kernel (paged_attn.cu)
+constexpr int PSM = 32;  // M tile rows
+constexpr int PSN = 32;  // key tile rows
+int paged_simt_grid(int r, int d_R, int dtype, int sms);  // blocks of its persistent grid (0 on error)
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
+
+struct PagedAppendArgs {
+  ChunkDev c;
+  PagesDev p;
+  MergeArgsDev m;
+  RopeTable rope;
+  const void* q_rope;
+  void* q_rope_out;
+  const float* tail_in;
+  float* tail_out;
+  int32_t *t_out, *cache_len;
+  void* row_state;
+  int32_t* dev_err;
+  int H, r, d_R, s;
+  int rotate;  // 0: keys and queries are rotated already
+  int tt;      // tokens of a block's tile
+};
+// The chunk window the append takes: a sequence that does not fit its table or
+// the P table (or has a negative time) takes none.
+using AppendWin = SeqWin;
+__device__ __forceinline__ AppendWin append_win(const PagedAppendArgs& a, int b, bool report) {
+  SeqWin w = seq_win(a.c, b);
+  if (w.n > 0) {
+    const int64_t j = group_of(w.t0 + w.n, a.s);
+    const bool cap = w.t0 < 0 || j > table_rows(a.p), pe = !cap && j > a.m.J_max;
+    if (cap || pe) {
+      if (report) set_err(a.dev_err, cap ? MTLA_DEVERR_CAPACITY : MTLA_DEVERR_PE_RANGE);
+      w.n = 0;
+    }
+  }
+  return w;
+}
+cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st);
+
+struct VerifyArgs {
+  int B, N, V;
+  const float *p, *q;
+  int64_t ld_p, ld_q;
+  const int32_t *tokens, *tok_start;
+  const float *u_accept, *u_sample;
+  int32_t *n_keep, *next_token;
+  int32_t* dev_err;
+};
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st);
+
+}  // namespace mtla

@@ -1,0 +1,272 @@
+// Appending a chunk of new tokens to a paged cache: the generic kernel (any
+// supported dims, fp32 or bf16 storage, fp32 arithmetic).
+//
+// What it computes (MTLA paper notes, "Key designs: hyper-network temporal
+// merging"): for every token, the gate w = sigmoid((c W_c + b_c) * P[j-1]), the
+// gated entry e = w * [c ; k^R] with k^R rotated to the token's position, and
+// the running sum of its group, S_t = S_{t-1} + e.
+//
+// The tokens of all sequences lie one after another in the token arrays, so a
+// block takes a tile of consecutive token rows whatever sequences they belong
+// to, and 32 of the row's D channels.  Its 256 threads split the r latents of
+// the gate contraction eight ways; a thread keeps its 1/8 of a channel's
+// column of W_c in registers for the whole tile, so W_c is read once a block.
+// A tile that begins inside a group starts that many tokens earlier (at most
+// s - 1) and recomputes their entries, so that no block waits for another; the
+// sums run from the group's start in token order in every tile, which makes
+// them independent of the tiling.  Few tokens: the chain of loads bounds it.
+#include "paged.cuh"
+
+namespace mtla {
+namespace pap {
+
+constexpr int NT = 256, NW = NT / 32;
+constexpr int U = 16;                // tokens of one round
+
+// One token's place, as the block's threads share it.
+struct Tok {
+  int64_t j;        // group (1-based)
+  int64_t prow;     // pool row to write, or -1
+  int seq;          // -1: no sequence takes this row
+  uint8_t opens;    // the running sum starts at this token's entry
+  uint8_t carry;    // ... or at tail_in plus it
+  uint8_t last;     // last token of its sequence's chunk
+  uint8_t out;      // stored by this block (not a recomputed one)
+};
+
+struct Smem {
+  float part[NW][U][32];
+  float v[U][32];       // gated entries, then sums
+  Tok tok[U];
+};
+
+// KPT: latents per warp, at least r / 8
+template <typename T, int KPT>
+__global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int gate_blocks,
+                                                          int rot_blocks) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int D = a.r + a.d_R, s = a.s;
+
+  if ((int)blockIdx.x >= gate_blocks + rot_blocks) {
+    // ---- per-sequence results: one warp a sequence
+    const int b = (blockIdx.x - gate_blocks - rot_blocks) * NW + warp;
+    if (b >= a.c.B) return;
+    const AppendWin w = append_win(a, b, lane == 0);
+    if (lane == 0) {
+      a.t_out[b] = (int32_t)(w.t0 + w.n);
+      if (a.cache_len) a.cache_len[b] = w.t0 + w.n > 0 ? (int32_t)group_of(w.t0 + w.n, s) : 0;
+    }
+    if (w.n == 0)
+      for (int k = lane; k < D; k += 32) a.tail_out[(int64_t)b * D + k] = a.tail_in[(int64_t)b * D + k];
+    return;
+  }
+  if ((int)blockIdx.x >= gate_blocks) {
+    // ---- RoPE queries: one warp a token, its d_R / 2 angles once for all heads
+    const int i = (blockIdx.x - gate_blocks) * NW + warp;
+    if (i >= a.c.N) return;
+    const int b = warp_find_seq(a.c.tok_start, a.c.B, i);
+    if (b < 0) return;
+    const AppendWin w = append_win(a, b, false);
+    if (i - w.first >= w.n) return;
+    const int64_t pos = w.t0 + (i - w.first);
+    const T* src = reinterpret_cast<const T*>(a.q_rope) + (int64_t)i * a.H * a.d_R;
+    T* dst = reinterpret_cast<T*>(a.q_rope_out) + (int64_t)i * a.H * a.d_R;
+    for (int k = lane; k < a.d_R / 2; k += 32) {
+      const float2 cs = a.rotate ? rope_cos_sin(pos, a.rope.turns[k]) : make_float2(1.f, 0.f);
+      for (int h = 0; h < a.H; ++h) {
+        const float x0 = ld_f32(src + h * a.d_R + 2 * k), x1 = ld_f32(src + h * a.d_R + 2 * k + 1);
+        st_elem(dst + h * a.d_R + 2 * k, x0 * cs.x - x1 * cs.y);
+        st_elem(dst + h * a.d_R + 2 * k + 1, x0 * cs.y + x1 * cs.x);
+      }
+    }
+    return;
+  }
+
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  float* cs = reinterpret_cast<float*>(smem_raw + sizeof(Smem));  // [U][8 KPT] latents of the round
+  const int slabs = (D + 31) / 32;
+  const int ch = (blockIdx.x % slabs) * 32 + lane;   // this thread's channel
+  const bool live = ch < D;
+  const int64_t i_beg = (int64_t)(blockIdx.x / slabs) * a.tt;
+  const int64_t i_end = i_beg + a.tt < a.c.N ? i_beg + a.tt : a.c.N;
+  float wv[KPT];
+#pragma unroll
+  for (int k = 0; k < KPT; ++k) {
+    const int kk = warp * KPT + k;
+    wv[k] = live && kk < a.r ? __ldg(a.m.W_c + (int64_t)kk * D + ch) : 0.f;
+  }
+  const float bc = live ? __ldg(a.m.b_c + ch) : 0.f;
+
+  // the tile's first group: recompute its earlier tokens of this chunk
+  int64_t i0 = i_beg;
+  {
+    const int b = warp_find_seq(a.c.tok_start, a.c.B, (int)i_beg);
+    if (b >= 0) {
+      const AppendWin w = append_win(a, b, false);
+      const int64_t place = i_beg - w.first;
+      if (place < w.n) {
+        const int64_t in_group = (w.t0 + place) % s;
+        i0 = i_beg - (in_group < place ? in_group : place);
+      }
+    }
+  }
+  float run = 0.f;  // (warp 0) the running sum of this thread's channel
+  for (int64_t r0 = i0; r0 < i_end; r0 += U) {
+    // places of the round's tokens: two a warp
+    for (int u = warp; u < U; u += NW) {
+      const int64_t i = r0 + u;
+      Tok t;
+      t.seq = -1;
+      t.j = 1;
+      t.prow = -1;
+      t.opens = t.carry = t.last = t.out = 0;
+      if (i < i_end) {
+        const int b = warp_find_seq(a.c.tok_start, a.c.B, (int)i);
+        if (b >= 0) {
+          const AppendWin w = append_win(a, b, false);
+          const int place = (int)(i - w.first);
+          if (place < w.n) {
+            const int64_t tm = w.t0 + place;  // 0-based time
+            t.seq = b;
+            t.j = tm / s + 1;
+            t.opens = tm % s == 0 || place == 0;
+            t.carry = tm % s != 0 && place == 0;
+            t.last = place + 1 == w.n;
+            t.out = i >= i_beg;
+            if (t.out && (t.last || (tm + 1) % s == 0)) {
+              t.prow = pool_row(a.p, b, t.j - 1);
+              if (t.prow < 0 && lane == 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+            }
+          }
+        }
+      }
+      if (lane == 0) sm.tok[u] = t;
+    }
+    for (int k = tid; k < U * (KPT * NW / 4); k += NT) {
+      const int u = k / (KPT * NW / 4), e = (k - u * (KPT * NW / 4)) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r0 + u < i_end && e < a.r) {
+        const T* src = reinterpret_cast<const T*>(a.m.c_new) + (r0 + u) * a.r + e;
+        v = make_float4(ld_f32(src), ld_f32(src + 1), ld_f32(src + 2), ld_f32(src + 3));
+      }
+      *reinterpret_cast<float4*>(cs + u * (KPT * NW) + e) = v;
+    }
+    __syncthreads();
+    {
+      float acc[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[u] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KPT; k += 4) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float4 c4 = *reinterpret_cast<const float4*>(cs + u * (KPT * NW) + warp * KPT + k);
+          acc[u] = fmaf(c4.x, wv[k], acc[u]);
+          acc[u] = fmaf(c4.y, wv[k + 1], acc[u]);
+          acc[u] = fmaf(c4.z, wv[k + 2], acc[u]);
+          acc[u] = fmaf(c4.w, wv[k + 3], acc[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sm.part[warp][u][lane] = acc[u];
+    }
+    __syncthreads();
+    for (int u = warp; u < U; u += NW) {  // gated entries
+      const Tok t = sm.tok[u];
+      float e = 0.f;
+      if (t.seq >= 0 && live) {
+        float g = bc;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) g += sm.part[w][u][lane];
+        const int64_t i = r0 + u;
+        float x;
+        if (ch < a.r) {
+          x = cs[u * (KPT * NW) + ch];
+        } else {
+          const T* kr = reinterpret_cast<const T*>(a.m.kR_new) + i * a.d_R;
+          const int k = ch - a.r;
+          x = ld_f32(kr + k);
+          if (a.rotate) {
+            const float y = ld_f32(kr + (k ^ 1));
+            const AppendWin w = append_win(a, t.seq, false);
+            const float2 r = rope_cos_sin(w.t0 + (i - w.first), a.rope.turns[k >> 1]);
+            x = (k & 1) ? y * r.y + x * r.x : x * r.x - y * r.y;
+          }
+        }
+        e = x * sigmoidf_(g * __ldg(a.m.P + (t.j - 1) * D + ch));
+      }
+      sm.v[u][lane] = e;
+    }
+    __syncthreads();
+    if (warp == 0) {  // running sums, in token order
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Tok t = sm.tok[u];
+        const float e = sm.v[u][lane];
+        if (t.seq >= 0) {
+          if (t.opens) run = t.carry && live ? a.tail_in[(int64_t)t.seq * D + ch] + e : e;
+          else run += e;
+        }
+        sm.v[u][lane] = run;
+      }
+    }
+    __syncthreads();
+    for (int u = warp; u < U; u += NW) {
+      const Tok t = sm.tok[u];
+      if (t.seq < 0 || !t.out || !live) continue;
+      const float v = sm.v[u][lane];
+      if (a.row_state) st_elem(reinterpret_cast<T*>(a.row_state) + (r0 + u) * D + ch, v);
+      if (t.prow >= 0) st_elem(reinterpret_cast<T*>(a.p.pages) + t.prow * a.p.row_stride + ch, v);
+      if (t.last) a.tail_out[(int64_t)t.seq * D + ch] = v;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T>
+static auto pick(int r) -> void (*)(const PagedAppendArgs, int, int) {
+  if (r <= 64) return paged_append_kernel<T, 8>;
+  if (r <= 256) return paged_append_kernel<T, 32>;
+  return paged_append_kernel<T, 64>;
+}
+
+}  // namespace pap
+
+cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st) {
+  const int D = a.r + a.d_R, slabs = (D + 31) / 32;
+  // Tile length: one round of 16 tokens while that does not give every SM its
+  // eight blocks, then longer (W_c is read once a block); and not below the
+  // stride, up to 512 tokens, so that a tile recomputes at most about its own
+  // length again.
+  int64_t rounds = cdiv((int64_t)a.c.N * slabs, (int64_t)pap::U * sms * 8);
+  rounds = rounds < 1 ? 1 : (rounds > 16 ? 16 : rounds);
+  int64_t tt = rounds * pap::U;
+  const int64_t up = cdiv(a.s < 512 ? a.s : 512, pap::U) * pap::U;
+  if (tt < up) tt = up;
+  a.tt = (int)tt;
+  const int kpt = a.r <= 64 ? 8 : (a.r <= 256 ? 32 : 64);
+  const size_t smem = sizeof(pap::Smem) + (size_t)pap::U * kpt * pap::NW * 4;
+  auto k = dtype == MTLA_BF16 ? pap::pick<__nv_bfloat16>(a.r) : pap::pick<float>(a.r);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t gate = cdiv(a.c.N, tt) * slabs;
+  const int64_t rot = a.q_rope ? cdiv(a.c.N, pap::NW) : 0;
+  const int64_t seq = cdiv(a.c.B, pap::NW);
+  if (gate + rot + seq >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(gate + rot + seq));
+  cfg.blockDim = dim3(pap::NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, (const PagedAppendArgs)a, (int)gate, (int)rot);
+}
+
+}  // namespace mtla

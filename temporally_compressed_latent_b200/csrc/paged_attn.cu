@@ -1,0 +1,391 @@
+// Attention of a chunk of new tokens over a paged cache: the generic kernel
+// (any supported H, r, d_R; fp32 or bf16 storage, fp32 arithmetic) and the
+// kernel that combines the parts of split items (shared with the tensor-core
+// kernel in paged_attn_tc.cu).
+//
+// What it computes (MTLA paper notes, "Key designs: stride-aware causal mask"
+// and "decoupled RoPE with temporal compression"; Figure 2(c) of the abstract
+// page): the query of a token at time t attends the complete groups before its
+// own (cache rows 0 .. ceil(t/s) - 2) and its own state row; one pass over the
+// columns with a running maximum and sum per row,
+//   m' = max(m, x),  l' = l 2^(m - m') + sum 2^(x - m'),  O' = O 2^(m - m') + P C_hat,
+// x in log2 units.  The own states are virtual key rows behind the cache rows,
+// so every row that is stored has at least one visible column.
+//
+// A block walks its share of the items (paged.cuh): 32 (token, head) rows of a
+// sequence against key tiles of 32 rows.  The scores take 2 x 2 per thread
+// from shared memory with float4 loads, the values 4 rows x 4 n channels per
+// thread with the running output in registers.  FFMA issue bounds it.
+#include "paged.cuh"
+
+namespace mtla {
+namespace psimt {
+
+constexpr int NT = 256;
+
+size_t smem_bytes(int D) { return (size_t)(PSM + PSN) * (D + 4) * 4 + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + 256 * 8 + sizeof(PlanShared) + sizeof(Item) + 64; }
+
+template <typename T> __device__ __forceinline__ void ld4(const T* p, float* v);
+template <> __device__ __forceinline__ void ld4<float>(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+template <> __device__ __forceinline__ void ld4<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+
+// NQ: channel quads per lane, ceil(r / 128)
+template <typename T, int NQ>
+__global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs a) {
+  extern __shared__ float smem[];
+  const int D = a.r + a.d_R, DP = D + 4;  // row pitch: float4 reads of 16 rows touch every bank group once
+  float* Qs = smem;                       // [PSM][DP]
+  float* Ks = Qs + PSM * DP;              // [PSN][DP]
+  float* Ss = Ks + PSN * DP;              // [PSN][PSM + 4]: probabilities, key-major
+  float* sm_m = Ss + PSN * (PSM + 4);     // [PSM] running maxima
+  float* sm_l = sm_m + PSM;               // [PSM] running sums
+  float* sm_a = sm_l + PSM;               // [PSM] rescale factors of the current tile
+  PlanShared* plan = reinterpret_cast<PlanShared*>((reinterpret_cast<uintptr_t>(sm_a + PSM) + 15) & ~uintptr_t(15));
+  Item* sit = reinterpret_cast<Item*>(plan + 1);
+  int* more = reinterpret_cast<int*>(sit + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int grid = gridDim.x, x = blockIdx.x;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  plan_block<NT>(a.c, a.p, a.plan, grid, x, a.dev_err, plan);
+  ItemWalk walk;
+  walk.hi = walk.pos = 0;
+  if (warp == 0) walk.init(a.c, a.p, a.plan, grid, x, plan);
+  SplitDesc desc = {0, 0, 0, 0, 0, 0};  // (warp 0)
+
+  for (;;) {
+    if (warp == 0) {
+      Item it;
+      const bool any = walk.next(a.c, a.p, a.plan, &it);
+      if (lane == 0) {
+        *more = any;
+        if (any) *sit = it;
+      }
+      if (any && it.slot >= 0 && it.kt1 == it.kt) {  // a split item ends here
+        desc.row0 = it.row0;
+        desc.ntok = it.ntok;
+        desc.first = first_block(a.plan, walk.C, walk.G, walk.item_start);
+        desc.C = walk.C;
+        desc.G = walk.G;
+      }
+    }
+    __syncthreads();
+    if (!*more) break;
+    const Item it = *sit;
+    const int live = it.ntok * a.H;
+    const int64_t R8 = (it.R + 7) / 8 * 8;
+    // queries (rows past the live ones: zeros)
+    for (int k = tid; k < PSM * (D / 4); k += NT) {
+      const int i = k / (D / 4), e = (k - i * (D / 4)) * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i < live) {
+        const int64_t row = (int64_t)it.row0 * a.H + i;
+        if (e < a.r) ld4(reinterpret_cast<const T*>(a.q_abs) + row * a.r + e, v);
+        else ld4(reinterpret_cast<const T*>(a.q_rope) + row * a.d_R + (e - a.r), v);
+      }
+      *reinterpret_cast<float4*>(Qs + i * DP + e) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    if (tid < PSM) {
+      sm_m[tid] = -INFINITY;
+      sm_l[tid] = 0.f;
+    }
+    float o[4][NQ * 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < NQ * 4; ++c) o[i][c] = 0.f;
+
+    for (int kt = it.kt0; kt < it.kt1; ++kt) {
+      const int64_t v0 = (int64_t)kt * PSN;  // first virtual row
+      // keys: cache rows, then the tokens' own states; rows between and behind them are zeros
+      for (int k = tid; k < PSN * (D / 4); k += NT) {
+        const int i = k / (D / 4), e = (k - i * (D / 4)) * 4;
+        const int64_t g = v0 + i;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (g < it.R) {
+          const int64_t pr = pool_row(a.p, it.b, g);
+          if (pr >= 0) ld4(reinterpret_cast<const T*>(a.p.pages) + pr * a.p.row_stride + e, v);
+          else if (e == 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+        } else if (g >= R8 && g - R8 < it.ntok) {
+          ld4(reinterpret_cast<const T*>(a.row_state) + (it.row0 + (g - R8)) * D + e, v);
+        }
+        *reinterpret_cast<float4*>(Ks + i * DP + e) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      __syncthreads();
+      // scores: rows r0, r0 + 16; keys c0, c0 + 16
+      const int r0 = tid >> 4, c0 = tid & 15;
+      float s00 = 0.f, s01 = 0.f, s10 = 0.f, s11 = 0.f;
+      for (int e = 0; e < D; e += 4) {
+        const float4 q0 = *reinterpret_cast<const float4*>(Qs + r0 * DP + e);
+        const float4 q1 = *reinterpret_cast<const float4*>(Qs + (r0 + 16) * DP + e);
+        const float4 k0 = *reinterpret_cast<const float4*>(Ks + c0 * DP + e);
+        const float4 k1 = *reinterpret_cast<const float4*>(Ks + (c0 + 16) * DP + e);
+        s00 = fmaf(q0.x, k0.x, s00); s00 = fmaf(q0.y, k0.y, s00); s00 = fmaf(q0.z, k0.z, s00); s00 = fmaf(q0.w, k0.w, s00);
+        s01 = fmaf(q0.x, k1.x, s01); s01 = fmaf(q0.y, k1.y, s01); s01 = fmaf(q0.z, k1.z, s01); s01 = fmaf(q0.w, k1.w, s01);
+        s10 = fmaf(q1.x, k0.x, s10); s10 = fmaf(q1.y, k0.y, s10); s10 = fmaf(q1.z, k0.z, s10); s10 = fmaf(q1.w, k0.w, s10);
+        s11 = fmaf(q1.x, k1.x, s11); s11 = fmaf(q1.y, k1.y, s11); s11 = fmaf(q1.z, k1.z, s11); s11 = fmaf(q1.w, k1.w, s11);
+      }
+      auto put = [&](int i, int c, float v) {
+        const int tok = i / a.H;
+        const int64_t g = v0 + c, seen = group_of(it.t + tok, a.plan.s) - 1;
+        const bool vis = g < seen || g == R8 + tok;
+        Ss[c * (PSM + 4) + i] = vis && tok < it.ntok ? v * a.scale_log2 : -INFINITY;
+      };
+      put(r0, c0, s00);
+      put(r0, c0 + 16, s01);
+      put(r0 + 16, c0, s10);
+      put(r0 + 16, c0 + 16, s11);
+      __syncthreads();
+      {  // softmax: eight lanes a row, four keys each
+        const int i = tid >> 3, k0 = tid & 7;
+        float xv[4], mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          xv[k] = Ss[(k0 + 8 * k) * (PSM + 4) + i];
+          mx = fmaxf(mx, xv[k]);
+        }
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mo = sm_m[i], mn = fmaxf(mo, mx), ref = mn == -INFINITY ? 0.f : mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = exp2f(xv[k] - ref);  // exp2f(-inf) = 0
+          Ss[(k0 + 8 * k) * (PSM + 4) + i] = p;
+          sum += p;
+        }
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        __syncwarp();
+        if (k0 == 0) {
+          const float f = exp2f(mo - ref);     // 0 while nothing was visible
+          sm_a[i] = f;
+          sm_m[i] = mn;
+          sm_l[i] = sm_l[i] * f + sum;
+        }
+      }
+      __syncthreads();
+      // values: this warp's rows 4 warp .. + 3, channels 4 lane + 128 q
+      if (4 * warp < live) {
+        const float4 f = *reinterpret_cast<const float4*>(sm_a + 4 * warp);
+        const float fa[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < NQ * 4; ++c) o[i][c] *= fa[i];
+#pragma unroll 4
+        for (int k = 0; k < PSN; ++k) {
+          const float4 p4 = *reinterpret_cast<const float4*>(Ss + k * (PSM + 4) + 4 * warp);
+          const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const int e = 4 * lane + 128 * q;
+            if (e < a.r) {
+              const float4 c4 = *reinterpret_cast<const float4*>(Ks + k * DP + e);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[i][4 * q] = fmaf(pv[i], c4.x, o[i][4 * q]);
+                o[i][4 * q + 1] = fmaf(pv[i], c4.y, o[i][4 * q + 1]);
+                o[i][4 * q + 2] = fmaf(pv[i], c4.z, o[i][4 * q + 2]);
+                o[i][4 * q + 3] = fmaf(pv[i], c4.w, o[i][4 * q + 3]);
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // the item's rows out: finished, or as a part
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * warp + i;
+      if (row < live) {
+        const float m = sm_m[row], l = sm_l[row];
+        if (it.slot < 0) {
+          const int64_t orow = (int64_t)it.row0 * a.H + row;
+          const float inv = 1.f / l;
+          if (a.lse && lane == 0) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const int e = 4 * lane + 128 * q;
+            if (e < a.r) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float v = o[i][4 * q + c] * inv;
+                if (a.out_f32) reinterpret_cast<float*>(a.out)[orow * a.r + e + c] = v;
+                else st_elem(reinterpret_cast<T*>(a.out) + orow * a.r + e + c, v);
+              }
+            }
+          }
+        } else {
+          const int64_t prow = (int64_t)it.slot * a.rows + row;
+          if (lane == 0) a.part.ml[prow] = make_float2(m, l);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const int e = 4 * lane + 128 * q;
+            if (e < a.r)
+              *reinterpret_cast<float4*>(a.part.o + prow * a.r + e) =
+                  make_float4(o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]);
+          }
+        }
+      }
+    }
+    __syncthreads();  // the item and its statistics have been read
+  }
+  if (tid == 0) a.part.desc[x] = desc;
+}
+
+// ----------------------------------------------------------------------------
+// Combine: block (g, y) finishes rows of the split item that ends in block g of
+// the attention grid: out = sum_x 2^(m_x - M) O_x / sum_x 2^(m_x - M) l_x over
+// its parts.  A thread takes four channels of a row; 256 threads take 4 rows at
+// once when parts are few, and one row with the parts split four ways when
+// they are many (a long cache under one token: latency of the loads bounds
+// it, eight in flight a thread).
+// ----------------------------------------------------------------------------
+constexpr int CNT = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(CNT) paged_combine_kernel(const PagedAttnArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.x;
+  const SplitDesc d = a.part.desc[g];
+  const int live = d.ntok * a.H;
+  if (live == 0) return;
+  __shared__ float red[4][64][5];
+  __shared__ float red_l[4];
+  const int parts = g - d.first + 1;  // every block between has one (their shares are not empty)
+  const int pg = parts > 16 ? 4 : 1;  // groups of parts
+  const int sub = threadIdx.x >> 6, q0 = threadIdx.x & 63;
+  const int grp = pg == 4 ? sub : 0;
+  const int rows_at_once = 4 / pg;
+  for (int r0 = blockIdx.y * rows_at_once; r0 < live; r0 += gridDim.y * rows_at_once) {
+    const int row = r0 + (pg == 4 ? 0 : sub);
+    const bool on = row < live;
+    const int64_t orow = (int64_t)d.row0 * a.H + row;
+    for (int e = 4 * q0; e < (a.r + 255) / 256 * 256; e += 256) {
+      float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (on && e < a.r) {
+        for (int k0 = grp; k0 < parts; k0 += 8 * pg) {
+          float2 ml[8];
+          float4 o[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int k = k0 + u * pg;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < parts) {
+              const int64_t prow = (int64_t)(2 * (d.first + k) + (k == 0 ? 1 : 0)) * a.rows + row;
+              ml[u] = a.part.ml[prow];
+              o[u] = *reinterpret_cast<const float4*>(a.part.o + prow * a.r + e);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float Mn = fmaxf(M, ml[u].x), ref = Mn == -INFINITY ? 0.f : Mn;
+            const float f0 = exp2f(M - ref), f1 = exp2f(ml[u].x - ref);
+            L = L * f0 + ml[u].y * f1;
+            // a part with nothing visible to this row holds no values of it
+            acc[0] = acc[0] * f0 + (f1 > 0.f ? o[u].x * f1 : 0.f);
+            acc[1] = acc[1] * f0 + (f1 > 0.f ? o[u].y * f1 : 0.f);
+            acc[2] = acc[2] * f0 + (f1 > 0.f ? o[u].z * f1 : 0.f);
+            acc[3] = acc[3] * f0 + (f1 > 0.f ? o[u].w * f1 : 0.f);
+            M = Mn;
+          }
+        }
+      }
+      if (pg == 4) {  // join the four groups (block-uniform branch)
+        __syncthreads();
+        red[sub][q0][0] = acc[0];
+        red[sub][q0][1] = acc[1];
+        red[sub][q0][2] = acc[2];
+        red[sub][q0][3] = acc[3];
+        red[sub][q0][4] = M;
+        if (q0 == 0) red_l[sub] = L;
+        __syncthreads();
+        if (sub == 0 && on && e < a.r) {
+          float Mt = -INFINITY;
+          for (int s = 0; s < 4; ++s) Mt = fmaxf(Mt, red[s][q0][4]);
+          L = 0.f;
+          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+          for (int s = 0; s < 4; ++s) {
+            const float f = exp2f(red[s][q0][4] - Mt);
+            L += red_l[s] * f;
+            for (int c = 0; c < 4; ++c) acc[c] += red[s][q0][c] * f;
+          }
+          M = Mt;
+        }
+      }
+      if (on && e < a.r && (pg == 1 || sub == 0)) {
+        const float inv = 1.f / L;
+        if (a.lse && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
+        if (a.out_f32) {
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.r + e) =
+              make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_elem(reinterpret_cast<T*>(a.out) + orow * a.r + e + c, acc[c] * inv);
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+static auto simt_kernel(int r) -> void (*)(const PagedAttnArgs) {
+  if (r <= 128) return paged_attn_simt_kernel<T, 1>;
+  if (r <= 256) return paged_attn_simt_kernel<T, 2>;
+  return paged_attn_simt_kernel<T, 4>;
+}
+
+}  // namespace psimt
+
+int paged_simt_grid(int r, int d_R, int dtype, int sms) {
+  auto k = dtype == MTLA_BF16 ? psimt::simt_kernel<__nv_bfloat16>(r) : psimt::simt_kernel<float>(r);
+  const size_t smem = psimt::smem_bytes(r + d_R);
+  int occ = 0;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, smem) != cudaSuccess || occ < 1) return 0;
+  return sms * (occ < 4 ? occ : 4);
+}
+
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st) {
+  auto k = dtype == MTLA_BF16 ? psimt::simt_kernel<__nv_bfloat16>(a.r) : psimt::simt_kernel<float>(a.r);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(psimt::NT);
+  cfg.dynamicSmemBytes = psimt::smem_bytes(a.r + a.d_R);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t rows = (int64_t)a.c.N * a.H < a.rows ? (int64_t)a.c.N * a.H : a.rows;
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(rows < 8 ? rows : 8));
+  cfg.blockDim = dim3(psimt::CNT);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return dtype == MTLA_BF16 ? cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<__nv_bfloat16>, a)
+                            : cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<float>, a);
+}
+
+}  // namespace mtla
