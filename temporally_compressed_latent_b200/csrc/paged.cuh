@@ -392,6 +392,17 @@ int paged_simt_grid(int r, int d_R, int dtype, int sms);  // blocks of its persi
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
 
+// tensor-core kernel (paged_attn_tc.cu): bf16, r = 256, d_R = 32
+constexpr int PTC_ROWS = 128;  // M tile rows
+constexpr int PTC_COLS = 64;   // key tile columns
+struct PagedAttnMaps {
+  CUtensorMap q;      // q_abs as {32, N H rows, 8 planes}, boxes of 8 rows
+  CUtensorMap qr;     // q_rope {32, N H rows}, boxes of 8 rows
+  CUtensorMap own;    // row_state {32, N, 9 planes}, boxes of 8 rows
+  CUtensorMap cache;  // pages {32, pool rows, 9 planes}, boxes of 8 rows
+};
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, const PagedAttnMaps& m, int grid, cudaStream_t st);
+
 struct PagedAppendArgs {
   ChunkDev c;
   PagesDev p;

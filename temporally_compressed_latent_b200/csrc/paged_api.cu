@@ -44,17 +44,38 @@ mtla_status cache_args(const mtla_dims* dims, const mtla_paged_cache* c, PagesDe
   return MTLA_OK;
 }
 
-// Blocks of the attention's persistent grid and rows of its M tiles.
+// The attention's kernel, the blocks of its persistent grid and the rows of
+// its M tiles.  The tensor-core kernel takes the widths its operand planes and
+// TMEM columns are laid out for; its one block an SM needs no query.
 struct AttnShape {
+  bool tc;
   int grid, rows;
 };
 AttnShape attn_shape(const mtla_dims* d) {
-  AttnShape s = {0, 0};
+  AttnShape s = {false, 0, 0};
   const int sms = current_device_sms();
   if (sms <= 0) return s;
-  s.grid = paged_simt_grid(d->r, d->d_R, d->dtype, sms);
-  s.rows = PSM;
+  s.tc = d->dtype == MTLA_BF16 && d->r == 256 && d->d_R == 32;
+  s.grid = s.tc ? sms : paged_simt_grid(d->r, d->d_R, d->dtype, sms);
+  s.rows = s.tc ? PTC_ROWS : PSM;
   return s;
+}
+
+// Rows of width 288 in bf16 (or the 256 latents of a query) as planes of 32
+// elements, boxes of 8 rows: a box lands as one operand group, plane by plane.
+bool row_groups_map(CUtensorMap* m, const void* base, int64_t rows, int64_t stride_bytes, int planes) {
+  const cuuint64_t d[3] = {32, (cuuint64_t)rows, (cuuint64_t)planes}, st[2] = {(cuuint64_t)stride_bytes, 64};
+  const cuuint32_t box[3] = {32, 8, (cuuint32_t)planes};
+  return encode_bf16_tiled_map(m, base, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool paged_maps(PagedAttnMaps* m, const PagedAttnArgs& a) {
+  const int64_t rows = (int64_t)a.c.N * a.H;
+  const cuuint64_t d[2] = {32, (cuuint64_t)rows}, st[1] = {64};
+  const cuuint32_t box[2] = {32, 8};
+  return row_groups_map(&m->q, a.q_abs, rows, 512, 8) &&
+         encode_bf16_tiled_map(&m->qr, a.q_rope, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
+         row_groups_map(&m->own, a.row_state, a.c.N, 576, 9) &&
+         row_groups_map(&m->cache, a.p.pages, a.p.num_pages * a.p.page_rows, a.p.row_stride * 2, 9);
 }
 
 }  // namespace
@@ -163,9 +184,15 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   const int tpt = sh.rows / dims->H;
   a.plan.s = dims->s;
   a.plan.tpt = tpt < 16 ? tpt : 16;
-  a.plan.q = PSN / 8;
+  a.plan.q = (sh.tc ? PTC_COLS : PSN) / 8;
   a.plan.item_cost = 2;
-  if (launch_paged_attn_simt(a, sh.grid, dims->dtype, cs) != cudaSuccess) return MTLA_ERR_CUDA;
+  if (sh.tc) {
+    PagedAttnMaps maps;
+    if (!paged_maps(&maps, a)) return MTLA_ERR_CUDA;
+    if (launch_paged_attn_tc(a, maps, sh.grid, cs) != cudaSuccess) return MTLA_ERR_CUDA;
+  } else if (launch_paged_attn_simt(a, sh.grid, dims->dtype, cs) != cudaSuccess) {
+    return MTLA_ERR_CUDA;
+  }
   return from_cuda(launch_paged_combine(a, sh.grid, dims->dtype, cs));
 }
 
