@@ -436,6 +436,14 @@ __device__ __forceinline__ AppendWin append_win(const PagedAppendArgs& a, int b,
 }
 cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st);
 
+// tensor-core kernel (paged_append_tc.cu): bf16, r = 256, d_R = 32, s <= 64
+constexpr int PTA_MAX_S = 64;
+struct PagedAppendMaps {
+  CUtensorMap c;   // c_new {256, N}, boxes of 64 x 128 rows, 128-byte swizzle
+  CUtensorMap kr;  // kR_new {32, N}, boxes of 128 rows
+};
+cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMaps& m, int sms, cudaStream_t st);
+
 struct VerifyArgs {
   int B, N, V;
   const float *p, *q;

@@ -78,6 +78,14 @@ bool paged_maps(PagedAttnMaps* m, const PagedAttnArgs& a) {
          row_groups_map(&m->cache, a.p.pages, a.p.num_pages * a.p.page_rows, a.p.row_stride * 2, 9);
 }
 
+// The append's tensor-core kernel: the widths its tiles are laid out for, groups
+// that fit beside half a tile, and enough tokens that its start (W_c into TMEM)
+// costs less than the generic kernel's arithmetic.
+constexpr int APPEND_TC_TOKENS = 256;
+bool append_tc(const mtla_dims* d, int32_t N) {
+  return d->dtype == MTLA_BF16 && d->r == 256 && d->d_R == 32 && d->s <= PTA_MAX_S && N >= APPEND_TC_TOKENS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,7 +149,17 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   a.s = dims->s;
   const int sms = current_device_sms();
   if (sms <= 0) return MTLA_ERR_CUDA;
-  return from_cuda(launch_paged_append_simt(a, dims->dtype, sms, static_cast<cudaStream_t>(stream)));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (append_tc(dims, chunk->N)) {
+    PagedAppendMaps maps;
+    const cuuint64_t dc[2] = {256, (cuuint64_t)chunk->N}, sc[1] = {512}, dk[2] = {32, (cuuint64_t)chunk->N}, sk[1] = {64};
+    const cuuint32_t bc[2] = {64, 128}, bk[2] = {32, 128};
+    if (!encode_bf16_tiled_map(&maps.c, merge->c_new, 2, dc, sc, bc, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_bf16_tiled_map(&maps.kr, merge->kR_new, 2, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MTLA_ERR_CUDA;
+    return from_cuda(launch_paged_append_tc(a, maps, sms, cs));
+  }
+  return from_cuda(launch_paged_append_simt(a, dims->dtype, sms, cs));
 }
 
 mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* chunk, const void* q_abs,

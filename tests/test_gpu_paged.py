@@ -46,7 +46,10 @@ def test_append(dims, s, page_rows):
     ([1] * 40, list(range(40)), 2, {}),
     ([300, 45], [2, 9], 5, TINY),
     ([1200], [3], 1200, TINY),
-], ids=["ragged", "s3", "s32", "s64", "s300", "decode40", "tiny", "onegroup"])
+    ([1] * 300 + [0] * 40 + [3, 2], [i % 70 for i in range(342)], 2, dict(H=12)),
+    ([255, 0, 258], [129, 5, 0], 1, dict(H=16)),
+    ([2] * 150, [i % 9 for i in range(150)], 4, dict(H=5)),
+], ids=["ragged", "s3", "s32", "s64", "s300", "decode40", "tiny", "onegroup", "decode300", "s1", "pairs"])
 def test_append_long(new, past, s, dims):
     b = Batch(new, past, s=s, page_rows=16, seed=77, **dims)
     b.check_append(b.append())
@@ -67,6 +70,15 @@ def test_append_options(dims):
     b.check_append(b.append(state=False))
     b = Batch(count=[4, 2, 0, -3], **kw)
     b.check_append(b.append())
+    # the same with tokens enough for the long-chunk kernel
+    kw = dict(kw, new=[150, 9, 200, 2])
+    for make in (dict(pad=8), dict(count=[90, 20, 0, 1])):
+        b = Batch(spare_tokens=5, **make, **kw)
+        b.check_append(b.append(q="count" in make))
+    b = Batch(**kw)
+    b.check_append(b.append(in_place=True))
+    b = Batch(**kw)
+    b.check_append(b.append(rope_base=0.0, state=False), rope_base=0.0)
 
 
 def test_append_far_position():
@@ -114,31 +126,32 @@ def test_append_in_pieces_and_taken_back(dims):
         assert torch.equal(back.d_pages[at][: back.D], few.d_pages[at][: few.D])
 
 
-def test_append_refuses_on_the_device():
+@pytest.mark.parametrize("more", [[], [1] * 300], ids=["few", "many"])
+def test_append_refuses_on_the_device(more):
     """Sequences that do not fit take nothing and say why; the others are not disturbed."""
-    new, past, s = [3, 3, 3, 3], [4, 30, 2, 5], 2
+    new, past, s = [3, 3, 3, 3] + more, [4, 30, 2, 5] + [6] * len(more), 2
+    t_more, n_more = [7] * len(more), [1] * len(more)
     b = Batch(new, past, s=s, page_rows=8, seed=8)
-    b.table_pages_full = b.table_pages
     # sequence 1 needs 17 rows: a table of two pages holds 16
     b.paged = mtla.paged_cache(b.d_pages, b.num_pages, b.pr, b.stride, b.d_table[:, :2].contiguous(), 2)
     o = b.append()
     torch.cuda.synchronize()
     assert int(b.err.item()) == mtla.DEVERR_CAPACITY
-    assert o["t"].tolist() == [7, 30, 5, 8]
-    b.check_append(o, take=[3, 0, 3, 3])
+    assert o["t"].tolist() == [7, 30, 5, 8] + t_more
+    b.check_append(o, take=[3, 0, 3, 3] + n_more)
     # the P table ends before sequence 1's groups
     b = Batch(new, past, s=s, page_rows=8, seed=8)
     b.d["P"] = b.d["P"][:10].contiguous()
     o = b.append()
     torch.cuda.synchronize()
     assert int(b.err.item()) == mtla.DEVERR_PE_RANGE
-    b.check_append(o, take=[3, 0, 3, 3])
+    b.check_append(o, take=[3, 0, 3, 3] + n_more)
     # a negative time
     b = Batch(new, past, s=s, page_rows=8, seed=8)
     b.t_prev[2] = -1
     o = b.append()
     torch.cuda.synchronize()
-    assert int(b.err.item()) == mtla.DEVERR_CAPACITY and o["t"].tolist() == [7, 33, -1, 8]
+    assert int(b.err.item()) == mtla.DEVERR_CAPACITY and o["t"].tolist() == [7, 33, -1, 8] + t_more
     # a table entry outside the pool: its rows are not written, the rest is
     for bad in (-1, 1 << 30):
         b = Batch(new, past, s=s, page_rows=8, seed=8)
