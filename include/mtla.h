@@ -544,7 +544,7 @@ size_t mtla_paged_workspace_bytes(const mtla_dims *dims, int32_t B, int32_t N, i
  *   one.  tokens [N] int32 (a draft outside [0, V) is dropped and sets
  *   MTLA_DEVERR_TOKEN), tok_start [B + 1] int32, u_accept [N] and u_sample [B]
  *   fp32 in [0, 1); n_keep, next_token [B] int32, written.
- *   1 <= V <= 2^24.  4-byte alignment is enough for every array.
+ *   1 <= V <= 2^22.  4-byte alignment is enough for every array.
  */
 #define MTLA_DEVERR_TOKEN 16 /* a token index outside the vocabulary */
 

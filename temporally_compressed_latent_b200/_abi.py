@@ -140,6 +140,8 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():  # the handle without building a stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 

@@ -205,7 +205,15 @@ bool encode_weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K) {
 
 namespace mtla {
 mtla_status check_call_dims(const mtla_dims* d) { return check_dims(d); }
-int current_device_sms() { return device_sms(); }
+int current_device_sms() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && cached[dev] > 0) return cached[dev];
+  const int n = device_sms();
+  if (dev < 64 && n > 0) cached[dev] = n;
+  return n;
+}
 bool encode_bf16_tiled_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
                            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   return encode_bf16_map(map, base, rank, dims, strides, box, swizzle);

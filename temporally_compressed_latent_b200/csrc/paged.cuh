@@ -6,6 +6,22 @@
 
 namespace mtla {
 
+// Division of 32-bit numbers by a divisor the host knows: floor(x / d) =
+// floor(x m / 2^64) with m = ceil(2^64 / d) (exact for every 32-bit x and d > 1).
+struct FastDiv {
+  uint64_t m;  // 0: d == 1
+  uint32_t d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  f.m = d > 1 ? ~uint64_t(0) / d + 1 : 0;
+  return f;
+}
+__device__ __forceinline__ uint32_t div32(uint32_t x, const FastDiv& f) {
+  return f.m ? (uint32_t)__umul64hi((uint64_t)x, f.m) : x;
+}
+
 struct ChunkDev {
   int B, N;
   const int32_t* tok_start;  // [B + 1]
@@ -17,6 +33,7 @@ struct PagesDev {
   int64_t num_pages, row_stride;
   const int32_t* table;      // [B, table_pages]
   int page_rows, table_pages;
+  FastDiv div_rows;          // by page_rows
 };
 
 // A sequence's part of a chunk: token rows [first, first + n) at times t0 + 1 .. t0 + n.
@@ -43,7 +60,7 @@ __device__ __forceinline__ int64_t table_rows(const PagesDev& p) { return (int64
 
 // Pool row of sequence b's cache row g, or -1 (table entry outside the pool).  g < table_rows.
 __device__ __forceinline__ int64_t pool_row(const PagesDev& p, int b, int64_t g) {
-  const int64_t k = g / p.page_rows;
+  const int64_t k = div32((uint32_t)g, p.div_rows);
   const int32_t page = p.table[(int64_t)b * p.table_pages + k];
   return page >= 0 && page < p.num_pages ? (int64_t)page * p.page_rows + (g - k * p.page_rows) : -1;
 }
@@ -69,21 +86,36 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* tok_start, int B, in
 
 // ----------------------------------------------------------------------------
 // RoPE angles: channel pair k turns by pos * base^(-2k/d_R).  The host passes
-// base^(-2k/d_R) / (2 pi), so the device needs one multiply in double, the
-// fraction of a turn (exact), and a single-precision sine and cosine of an
-// angle within half a turn: the angle of position 2^31 is as exact as that of
-// position 1 (absolute error near 2^-24 of a half turn).
+// the angle of one position as a fraction of a turn in 64-bit fixed point (its
+// whole turns drop out), so the product with a position below 2^32 wraps to the
+// position's own fraction with an error below 2^-32 of a turn, by two integer
+// multiplies; its upper 32 bits give the quarter turn and the rest, whose sine
+// and cosine are short polynomials (error below 2^-23).  The angle of position
+// 2^31 is as exact as that of position 1.
 // ----------------------------------------------------------------------------
 constexpr int MAX_ROPE_PAIRS = 288;
 struct RopeTable {
-  double turns[MAX_ROPE_PAIRS];
+  uint64_t turns[MAX_ROPE_PAIRS];
 };
-__device__ __forceinline__ float2 rope_cos_sin(int64_t pos, double turns) {
-  const double a = (double)pos * turns;
-  const float f = (float)(a - rint(a));
-  float2 r;
-  sincospif(2.f * f, &r.y, &r.x);
-  return r;  // x = cos, y = sin
+__device__ __forceinline__ float2 rope_cos_sin(uint32_t pos, uint64_t turns) {
+  const uint32_t f = (uint32_t)((uint64_t)(pos * turns) >> 32);  // fraction of a turn, 2^-32 units
+  const uint32_t quarter = (f + (1u << 29)) >> 30;               // nearest quarter turn (mod 4)
+  // the rest, |y| <= pi / 4: Taylor polynomials to y^9 and y^8 (next terms
+  // below 2e-9 and 3e-8)
+  const float y = (float)(int32_t)(f - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const float z = y * y;
+  float sn = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  sn = fmaf(z, sn, 1.f / 120.f);
+  sn = fmaf(z, sn, -1.f / 6.f);
+  sn = fmaf(z * y, sn, y);
+  float cn = fmaf(z, 1.f / 40320.f, -1.f / 720.f);
+  cn = fmaf(z, cn, 1.f / 24.f);
+  cn = fmaf(z, cn, -0.5f);
+  cn = fmaf(z, cn, 1.f);
+  const float c = quarter & 1 ? sn : cn, s = quarter & 1 ? cn : sn;
+  // x = cos, y = sin of the whole angle: signs by quarter
+  return make_float2(__uint_as_float(__float_as_uint(c) ^ (((quarter + 1) & 2) << 30)),
+                     __uint_as_float(__float_as_uint(s) ^ ((quarter & 2) << 30)));
 }
 
 // ----------------------------------------------------------------------------
@@ -416,22 +448,27 @@ struct PagedAppendArgs {
   void* row_state;
   int32_t* dev_err;
   int H, r, d_R, s;
+  FastDiv div_s;
   int rotate;  // 0: keys and queries are rotated already
   int tt;      // tokens of a block's tile
 };
 // The chunk window the append takes: a sequence that does not fit its table or
-// the P table (or has a negative time) takes none.
+// the P table (or has a negative time) takes none.  Times of a chunk are below
+// 2^32, so divisions by s are 32-bit.
 using AppendWin = SeqWin;
-__device__ __forceinline__ AppendWin append_win(const PagedAppendArgs& a, int b, bool report) {
-  SeqWin w = seq_win(a.c, b);
+__device__ __forceinline__ void append_fit(const PagedAppendArgs& a, AppendWin& w, bool report) {
   if (w.n > 0) {
-    const int64_t j = group_of(w.t0 + w.n, a.s);
-    const bool cap = w.t0 < 0 || j > table_rows(a.p), pe = !cap && j > a.m.J_max;
+    const uint32_t j = div32((uint32_t)w.t0 + (uint32_t)w.n - 1u, a.div_s) + 1u;  // (of a t0 >= 0)
+    const bool cap = w.t0 < 0 || j > table_rows(a.p), pe = !cap && j > (uint32_t)a.m.J_max;
     if (cap || pe) {
       if (report) set_err(a.dev_err, cap ? MTLA_DEVERR_CAPACITY : MTLA_DEVERR_PE_RANGE);
       w.n = 0;
     }
   }
+}
+__device__ __forceinline__ AppendWin append_win(const PagedAppendArgs& a, int b, bool report) {
+  SeqWin w = seq_win(a.c, b);
+  append_fit(a, w, report);
   return w;
 }
 cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st);

@@ -41,6 +41,7 @@ mtla_status cache_args(const mtla_dims* dims, const mtla_paged_cache* c, PagesDe
   d->table = c->block_table;
   d->page_rows = c->page_rows;
   d->table_pages = c->table_pages;
+  d->div_rows = fast_div((uint32_t)c->page_rows);
   return MTLA_OK;
 }
 
@@ -133,8 +134,11 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   a.m.J_max = merge->J_max;
   a.rotate = rope_base > 0.0 && dims->d_R > 0;
   if (a.rotate)
-    for (int k = 0; k < dims->d_R / 2; ++k)
-      a.rope.turns[k] = pow(rope_base, -2.0 * k / dims->d_R) / 6.283185307179586476925;
+    for (int k = 0; k < dims->d_R / 2; ++k) {
+      const long double turn = powl((long double)rope_base, -2.0L * k / dims->d_R) / 6.283185307179586476925286766559L;
+      const long double part = turn - floorl(turn);  // in [0, 1)
+      a.rope.turns[k] = (uint64_t)(part * 18446744073709551616.0L);
+    }
   a.q_rope = dims->d_R > 0 ? q_rope : nullptr;
   a.q_rope_out = q_rope_out;
   a.tail_in = tail_in;
@@ -147,6 +151,7 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   a.r = dims->r;
   a.d_R = dims->d_R;
   a.s = dims->s;
+  a.div_s = fast_div((uint32_t)dims->s);
   const int sms = current_device_sms();
   if (sms <= 0) return MTLA_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -218,7 +223,7 @@ mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, 
                                int64_t ld_q, const int32_t* tokens, const int32_t* tok_start, const float* u_accept,
                                const float* u_sample, int32_t* n_keep, int32_t* next_token, int32_t* dev_err,
                                void* stream) {
-  if (B < 0 || N < 0 || V < 1 || V > (1 << 24) || ld_p < V || (q && ld_q < V)) return MTLA_ERR_INVALID_ARG;
+  if (B < 0 || N < 0 || V < 1 || V > (1 << 22) || ld_p < V || (q && ld_q < V)) return MTLA_ERR_INVALID_ARG;
   if (!p || !tokens || !tok_start || !u_accept || !u_sample || !n_keep || !next_token || !dev_err)
     return MTLA_ERR_INVALID_ARG;
   const void* ptrs[] = {p, q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err};

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
     if (b < 0) return;
     const AppendWin w = append_win(a, b, false);
     if (i - w.first >= w.n) return;
-    const int64_t pos = w.t0 + (i - w.first);
+    const uint32_t pos = (uint32_t)(w.t0 + (i - w.first));
     const T* src = reinterpret_cast<const T*>(a.q_rope) + (int64_t)i * a.H * a.d_R;
     T* dst = reinterpret_cast<T*>(a.q_rope_out) + (int64_t)i * a.H * a.d_R;
     for (int k = lane; k < a.d_R / 2; k += 32) {
@@ -129,14 +129,15 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
           const AppendWin w = append_win(a, b, false);
           const int place = (int)(i - w.first);
           if (place < w.n) {
-            const int64_t tm = w.t0 + place;  // 0-based time
+            const uint32_t tm = (uint32_t)(w.t0 + place);  // 0-based time
+            const uint32_t g = div32(tm, a.div_s), in = tm - g * (uint32_t)s;
             t.seq = b;
-            t.j = tm / s + 1;
-            t.opens = tm % s == 0 || place == 0;
-            t.carry = tm % s != 0 && place == 0;
+            t.j = (int64_t)g + 1;
+            t.opens = in == 0 || place == 0;
+            t.carry = in != 0 && place == 0;
             t.last = place + 1 == w.n;
             t.out = i >= i_beg;
-            if (t.out && (t.last || (tm + 1) % s == 0)) {
+            if (t.out && (t.last || in + 1 == (uint32_t)s)) {
               t.prow = pool_row(a.p, b, t.j - 1);
               if (t.prow < 0 && lane == 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
             }
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
           if (a.rotate) {
             const float y = ld_f32(kr + (k ^ 1));
             const AppendWin w = append_win(a, t.seq, false);
-            const float2 r = rope_cos_sin(w.t0 + (i - w.first), a.rope.turns[k >> 1]);
+            const float2 r = rope_cos_sin((uint32_t)(w.t0 + (i - w.first)), a.rope.turns[k >> 1]);
             x = (k & 1) ? y * r.y + x * r.x : x * r.x - y * r.y;
           }
         }
@@ -250,8 +251,19 @@ cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cud
   const int kpt = a.r <= 64 ? 8 : (a.r <= 256 ? 32 : 64);
   const size_t smem = sizeof(pap::Smem) + (size_t)pap::U * kpt * pap::NW * 4;
   auto k = dtype == MTLA_BF16 ? pap::pick<__nv_bfloat16>(a.r) : pap::pick<float>(a.r);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  {
+    // the shared-memory opt-in, once per instance and device
+    static uint64_t done_mask[6] = {};
+    const int slot = (dtype == MTLA_BF16 ? 3 : 0) + (kpt == 8 ? 0 : (kpt == 32 ? 1 : 2));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done_mask[slot] & (1ull << dev))) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) done_mask[slot] |= 1ull << dev;
+    }
+  }
   const int64_t gate = cdiv(a.c.N, tt) * slabs;
   const int64_t rot = a.q_rope ? cdiv(a.c.N, pap::NW) : 0;
   const int64_t seq = cdiv(a.c.B, pap::NW);

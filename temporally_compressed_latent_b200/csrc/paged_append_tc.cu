@@ -19,14 +19,19 @@
 //    the previous tile's last ones: a group that began there is summed again
 //    from its start, so no CTA waits for another, and sums run in token order
 //    from the group's start everywhere.
-//  * A metadata warp works one tile ahead: it finds the tokens' sequences and
-//    leaves, per token, its P row, its pool row (if it closes a group or its
-//    chunk), its position and flags in shared memory.  The epilogue loads P and
-//    the open groups' tails one chunk of 16 tokens ahead of their use.
-//  * RoPE: an exact angle (double) every 8 tokens of a sequence and a rotation
-//    by the pair's own angle between them (at most 7 single-precision
-//    products: error below 2^-20 of the key).  The queries are rotated by the
-//    epilogue warps while W_c and the first tiles are on their way.
+//  * Two metadata warps work a tile ahead: they find the tokens' sequences and
+//    leave P rows, pool rows, positions and bit masks (which tokens open a
+//    group, end a chunk, ...) in shared memory, and send the tile's P rows
+//    towards L2.  The epilogue's 12 warps take 32 columns each in chunks of 16;
+//    they are bound by issue and by the latency of their chain, so P comes to
+//    shared memory by asynchronous copies while the tile before is stored, and
+//    finished rows leave through a staging block, 16 bytes of eight rows a step.
+//  * RoPE: an exact angle every 8 tokens of a run of positions and a rotation
+//    by the pair's own angle between them (at most seven single-precision
+//    products: error below 2^-20 of the key).
+//  * The queries are a stream of their own (no tile needs them): a second,
+//    small kernel rotates them on the registers that this one leaves free, on
+//    the same SMs at the same time.
 #include "paged.cuh"
 
 namespace mtla {
@@ -40,33 +45,39 @@ constexpr int BBLK = NTOK * 128;               // one K block of a tile: 16384 B
 constexpr int KS = 2 * KB;                     // stages: two tiles
 constexpr int KRBLK = NTOK * DR * 2;           // RoPE keys of a tile: 8192 B
 constexpr int NWARPS = 16, NT = 32 * NWARPS;
-constexpr int NEPI = 12;                       // epilogue warps: four per live lane quarter
-constexpr int TMA_WARP = 3, MMA_WARP = 7, META_WARP = 11, SEQ_WARP = 15;  // warps of the padding quarter
+constexpr int NPART = NWARPS / 4, PCOL = NTOK / NPART;  // column parts of a tile (4) and their columns (32)
+constexpr int NEPI = 3 * NPART;                // epilogue warps
+constexpr int TMA_WARP = 3, MMA_WARP = 7, META_WARP0 = 11, META_WARP1 = 15;  // warps of the padding quarter
 constexpr uint32_t TMEM_COLS = 512, ACC_STRIDE = 128, HI_COL = 256, LO_COL = 384;
 constexpr uint32_t IDESC = umma_idesc_bf16(M, NTOK, false, false);
 
-// flags of a token
-constexpr int F_TAKEN = 1;   // a sequence takes it
-constexpr int F_OPEN = 2;    // the sum starts here (at tail_in with F_CARRY)
-constexpr int F_CARRY = 4;
-constexpr int F_LAST = 8;    // last token of its chunk
-constexpr int F_BACK = 8;    // shift of: tokens of its group in the chunk before it
-
+// What the epilogue needs to know of a tile's tokens.
 struct Meta {
-  int4 tok[NTOK];   // P row, pool row or -1, position, flags
+  int prow[NTOK];       // P row
+  int pool[NTOK];       // pool row of a token that writes one
+  uint32_t pos[NTOK];   // position (0-based time)
   int seq[NTOK];
+  int back[NTOK];       // tokens of its group in the chunk before it
+  uint32_t taken[4];    // bit l of word m: token 32 m + l.  A sequence takes it
+  uint32_t open[4];     // the sum starts here (with a carry: at tail_in)
+  uint32_t carry[4];
+  uint32_t last[4];     // last token of its chunk
+  uint32_t row[4];      // it writes a cache row
+  uint32_t turn[4];     // its position is not the previous token's plus one
 };
 
 constexpr size_t OFF_B = 0;
 constexpr size_t OFF_KR = OFF_B + (size_t)KS * BBLK;
 constexpr size_t OFF_META = OFF_KR + 2 * (size_t)KRBLK;
-constexpr size_t OFF_ROPE = OFF_META + 2 * sizeof(Meta);
+constexpr size_t OFF_OST = (OFF_META + 2 * sizeof(Meta) + 127) / 128 * 128;  // staged rows: 2 KB an epilogue warp
+constexpr size_t OFF_P = OFF_OST + (size_t)NEPI * PCOL * 64;  // P of a tile: 32 columns x 32 channels a warp, fp32
+constexpr size_t OFF_ROPE = OFF_P + (size_t)NEPI * PCOL * 128;
 constexpr size_t OFF_BAR = OFF_ROPE + (DR / 2) * 8;
 constexpr int NBAR = 2 * KS + 2 * 4 + 1;
 constexpr size_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr size_t SMEM = OFF_TMEM + 16 + 1024;
 static_assert(SMEM <= 232448, "one block's shared memory (227 KB)");
-static_assert(sizeof(Meta) % 16 == 0 && OFF_META % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(OFF_ROPE % 8 == 0 && sizeof(Meta) % 16 == 0 && OFF_META % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -116,57 +127,63 @@ __device__ __forceinline__ void warp_sequences(const ChunkDev& c, int64_t base, 
   }
 }
 
-// Rotate the queries of 32 token rows (or fewer) by one warp: lane l first finds
-// row base + l's position; then two tokens a round, the 16 angles of each by
-// one half of the warp, 16 bytes of a token a lane and step.
-__device__ void rotate_queries(const PagedAppendArgs& a, int64_t base, int rows, const double* turns) {
-  const int lane = threadIdx.x & 31;
-  int b[1];
-  warp_sequences<1>(a.c, base, b);
-  int64_t pos = -1;
-  if (lane < rows && base + lane < a.c.N && b[0] >= 0) {
-    const AppendWin w = append_win(a, b[0], false);
-    const int64_t place = base + lane - w.first;
-    if (place < w.n) pos = w.t0 + place;
-  }
-  const int words = a.H * (DR / 8);  // 16-byte pieces of a token
-  const uint4* src = reinterpret_cast<const uint4*>(a.q_rope);
-  uint4* dst = reinterpret_cast<uint4*>(a.q_rope_out);
-  for (int k = 0; k < rows; k += 2) {
-    const int64_t p0 = __shfl_sync(0xffffffffu, pos, k), p1 = __shfl_sync(0xffffffffu, pos, k + 1 < 32 ? k + 1 : 31);
-    const int64_t p[2] = {p0, k + 1 < rows ? p1 : -1};
-    if (p[0] < 0 && p[1] < 0) continue;
-    const int64_t mine = lane < 16 ? p[0] : p[1];
-    const float2 cs = a.rotate ? rope_cos_sin(mine < 0 ? 0 : mine, turns[lane & 15]) : make_float2(1.f, 0.f);
-    for (int w0 = 0; w0 < words; w0 += 32) {
-      const int word = w0 + lane;
+// Rotates the queries: a warp takes QROWS token rows, all their loads in flight
+// before the first angle; a half of the warp computes a token's 16 angles, a
+// lane turns 16 bytes of a row.  It reads nothing that the append kernel
+// writes, so it starts as soon as that one has started (by then everything
+// before both is complete) and waits for it only at its end, so that what
+// follows finds both done.
+constexpr int QROWS = 4, QT = 256;
+__global__ void __launch_bounds__(QT, 4) paged_rotate_kernel(const __grid_constant__ PagedAppendArgs a) {
+  const int lane = threadIdx.x & 31, words = a.H * (DR / 8);
+  const int64_t i = ((int64_t)blockIdx.x * (QT / 32) + (threadIdx.x >> 5)) * QROWS;
+  if (i < a.c.N) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.q_rope);
+    uint4* dst = reinterpret_cast<uint4*>(a.q_rope_out);
+    const uint64_t turn = a.rotate ? a.rope.turns[lane & 15] : 0;
+    int b[1];
+    warp_sequences<1>(a.c, i, b);
+    AppendWin w = seq_win(a.c, b[0] < 0 ? 0 : b[0]);
+    append_fit(a, w, false);
+    const int64_t place = i + lane - w.first;
+    const uint32_t taken =
+        __ballot_sync(0xffffffffu, lane < QROWS && i + lane < a.c.N && b[0] >= 0 && place >= 0 && place < w.n);
+    const uint32_t pos = (uint32_t)w.t0 + (uint32_t)place;
+    for (int word = lane; word < (words + 31) / 32 * 32; word += 32) {
+      uint4 v[QROWS];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = (base + k + h) * words + word;
-        const bool on = p[h] >= 0 && word < words;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = src[at];
-        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int k = 0; k < QROWS; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if ((taken >> k & 1) && word < words) v[k] = src[(i + k) * words + word];
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // pair 4 (word mod 4) + e
-          const int sl = 16 * h + 4 * (word & 3) + e;
-          const float co = __shfl_sync(0xffffffffu, cs.x, sl), si = __shfl_sync(0xffffffffu, cs.y, sl);
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
-          x[e] = pack_bf16x2(f.x * co - f.y * si, f.x * si + f.y * co);
+      for (int k = 0; k < QROWS; k += 2) {
+        const float2 cs = rope_cos_sin(__shfl_sync(0xffffffffu, pos, k + (lane >> 4)), turn);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[4] = {v[k + h].x, v[k + h].y, v[k + h].z, v[k + h].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {          // pair 4 (word mod 4) + e
+            const int sl = 16 * h + 4 * (word & 3) + e;
+            const float co = __shfl_sync(0xffffffffu, cs.x, sl), si = __shfl_sync(0xffffffffu, cs.y, sl);
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+            x[e] = pack_bf16x2(f.x * co - f.y * si, f.x * si + f.y * co);
+          }
+          if ((taken >> (k + h) & 1) && word < words) dst[(i + k + h) * words + word] = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        if (on) dst[at] = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_constant__ PagedAppendMaps mp,
+__global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ PagedAppendMaps mp,
                                                                 const __grid_constant__ PagedAppendArgs a, int n_tiles) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   uint64_t* const k_full = bar;                  // [KS]
-  uint64_t* const k_empty = bar + KS;            // [KS]
+  uint64_t* const k_empty = bar + KS;            // [2] a tile's stages (epilogue)
   uint64_t* const acc_full = bar + 2 * KS;       // [2]
   uint64_t* const acc_empty = acc_full + 2;      // [2]
   uint64_t* const meta_full = acc_full + 4;      // [2]
@@ -174,39 +191,31 @@ __global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_con
   uint64_t* const mma_done = acc_full + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
   Meta* meta = reinterpret_cast<Meta*>(sm + OFF_META);
-  double* turns = reinterpret_cast<double*>(sm + OFF_ROPE);
+  uint64_t* turns = reinterpret_cast<uint64_t*>(sm + OFF_ROPE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ct = blockIdx.x % CT, G = gridDim.x / CT, j0 = blockIdx.x / CT;
   const int u_beg = (int)((int64_t)j0 * n_tiles / G), u_end = (int)((int64_t)(j0 + 1) * n_tiles / G);
   const bool has_rope = (ct + 1) * NCT > R;
   const int s = a.s, halo = s - 1, nout = NTOK - halo;
-  const int q = warp & 3, part = warp >> 2;      // TMEM lane quarter; quarter of the tile's tokens
+  const int q = warp & 3, part = warp >> 2;      // TMEM lane quarter; eighth of the tile's columns
   const bool epi = q < 3;
   const int ch = ct * NCT + q * 32 + lane;       // this thread's channel (epilogue warps)
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // W_c^T: all of its loads in flight before anything else
-  float wv[64];
-  if (epi) {
-#pragma unroll
-    for (int k = 0; k < 64; ++k) wv[k] = __ldg(a.m.W_c + (size_t)(64 * part + k) * D + ch);
-  }
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], NEPI);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_empty[i], NEPI);
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], NEPI);
-      mbar_init(&meta_full[i], 1);
+      mbar_init(&meta_full[i], 2);
       mbar_init(&meta_empty[i], NEPI);
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
   }
-  if (tid < DR / 2) turns[tid] = a.rotate ? a.rope.turns[tid] : 0.0;
+  if (tid < DR / 2) turns[tid] = a.rotate ? a.rope.turns[tid] : 0;  // (no rotation: by nothing)
   if (warp == 0) {
     tmem_alloc(tmem_holder, TMEM_COLS);
     tmem_relinquish();
@@ -214,6 +223,15 @@ __global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_con
   if (warp == TMA_WARP && lane == 0) {
     prefetch_tmap(&mp.c);
     prefetch_tmap(&mp.kr);
+  }
+  // (the query kernel may start once all before this call is complete)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // W_c^T: all of its loads in flight before anything else
+  float wv[64];
+  if (epi) {
+#pragma unroll
+    for (int k = 0; k < 64; ++k) wv[k] = __ldg(a.m.W_c + (size_t)(64 * part + k) * D + ch);
   }
   tc_fence_before();
   __syncthreads();
@@ -227,10 +245,10 @@ __global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_con
       uint32_t kc = 0;
       for (int u = u_beg; u < u_end && ok; ++u) {
         const int32_t row = u * nout - halo;     // (rows before the first and past the last are zeros)
-        const int b2 = ((u - u_beg) & 1);
+        const int b2 = (u - u_beg) & 1;
+        if (u - u_beg >= 2 && !mbar_wait(&k_empty[b2], (((u - u_beg) >> 1) & 1) ^ 1)) { ok = false; break; }
         for (int kb = 0; kb < KB; ++kb, ++kc) {
           const int st = kc % KS;
-          if (kc >= (uint32_t)KS && !mbar_wait(&k_empty[st], ((kc / KS) & 1) ^ 1)) { ok = false; break; }
           const bool kr = has_rope && kb == 0;   // the tile's RoPE keys ride with its first block
           mbar_arrive_expect_tx(&k_full[st], BBLK + (kr ? KRBLK : 0));
           tma_load_2d(sm + OFF_B + st * BBLK, &mp.c, kb * 64, row, &k_full[st]);
@@ -273,69 +291,104 @@ __global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_con
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
     warp_wait(mma_done, 0);
-  } else if (warp == META_WARP) {
-    // ======================= token metadata, one tile ahead =======================
+  } else if (warp == META_WARP0 || warp == META_WARP1) {
+    // ======================= token metadata, one tile ahead: 64 tokens a warp =======================
+    const int m0 = warp == META_WARP0 ? 0 : 2;
     uint32_t tc = 0;
     for (int u = u_beg; u < u_end; ++u, ++tc) {
       const int mb = tc & 1;
       const int64_t base = (int64_t)u * nout - halo;
-      int b[4];
-      warp_sequences<4>(a.c, base, b);
-      int4 t[4];
+      int b[2];
+      warp_sequences<2>(a.c, base + 32 * m0, b);
+      // windows of both tokens of a lane, then their table entries: two
+      // round trips a tile
+      AppendWin w[2];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int64_t i = base + lane + 32 * m;
-        t[m] = make_int4(0, -1, 0, 0);
-        if (b[m] >= 0 && i >= 0 && i < a.c.N) {
-          const AppendWin w = append_win(a, b[m], false);
-          const int64_t place = i - w.first;
-          if (place >= 0 && place < w.n) {
-            const int64_t tm = w.t0 + place;     // 0-based time
-            const int in = (int)(tm % s);
-            const int64_t g = tm / s;
-            t[m].x = (int)g;
-            t[m].z = (int)tm;
-            const bool last = place + 1 == w.n;
-            t[m].w = F_TAKEN | (in == 0 || place == 0 ? F_OPEN : 0) | (in != 0 && place == 0 ? F_CARRY : 0) |
-                     (last ? F_LAST : 0) | ((int)(in < place ? in : place) << F_BACK);
-            if ((last || in + 1 == s) && lane + 32 * m >= halo) {
-              t[m].y = (int)pool_row(a.p, b[m], g);
-              if (t[m].y < 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
-            }
-          }
-        }
+      for (int m = 0; m < 2; ++m) w[m] = seq_win(a.c, b[m] < 0 ? 0 : b[m]);
+      uint32_t pos[2], grp[2];
+      int back[2];
+      uint32_t fl[2];
+      const int32_t* entry[2];
+      int slot[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        append_fit(a, w[m], false);
+        const int64_t i = base + lane + 32 * (m0 + m), place = i - w[m].first;
+        const bool taken = b[m] >= 0 && i >= 0 && place >= 0 && place < w[m].n;
+        const uint32_t tm = taken ? (uint32_t)w[m].t0 + (uint32_t)place : 0;  // 0-based time
+        const uint32_t g = div32(tm, a.div_s), in = tm - g * (uint32_t)s;
+        const bool last = taken && place + 1 == w[m].n;
+        pos[m] = tm;
+        grp[m] = g;
+        back[m] = taken ? (int)(in < place ? (int64_t)in : place) : 0;
+        const bool row = taken && (last || in + 1 == (uint32_t)s) && lane + 32 * (m0 + m) >= halo;
+        fl[m] = (taken ? 1u : 0u) | (taken && (in == 0 || place == 0) ? 2u : 0u) | (taken && in != 0 && place == 0 ? 4u : 0u) |
+                (last ? 8u : 0u) | (row ? 16u : 0u);
+        const uint32_t k = div32(g, a.p.div_rows);
+        entry[m] = row ? a.p.table + (int64_t)b[m] * a.p.table_pages + k : nullptr;
+        slot[m] = (int)(g - k * (uint32_t)a.p.page_rows);
       }
+      // the tile's P rows (this CTA's channels) towards L2, a tile ahead of their use
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if ((fl[m] & 3) == 3 || (fl[m] & 1 && lane + 32 * (m0 + m) == 0)) {
+          const float* row = a.m.P + (int64_t)grp[m] * D + ct * NCT;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 32 * k));
+        }
+      int32_t page[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) page[m] = entry[m] ? *entry[m] : -1;
       if (tc >= 2 && !warp_wait(&meta_empty[mb], ((tc >> 1) & 1) ^ 1)) { ok = false; break; }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        meta[mb].tok[lane + 32 * m] = t[m];
-        meta[mb].seq[lane + 32 * m] = b[m];
+      for (int m = 0; m < 2; ++m) {
+        const bool in_pool = page[m] >= 0 && page[m] < a.p.num_pages;
+        if (entry[m] && !in_pool) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+        Meta& mt = meta[mb];
+        mt.prow[lane + 32 * (m0 + m)] = (int)grp[m];
+        mt.pool[lane + 32 * (m0 + m)] = in_pool ? page[m] * a.p.page_rows + slot[m] : -1;
+        mt.pos[lane + 32 * (m0 + m)] = pos[m];
+        mt.seq[lane + 32 * (m0 + m)] = b[m];
+        mt.back[lane + 32 * (m0 + m)] = back[m];
+        const uint32_t taken = __ballot_sync(0xffffffffu, fl[m] & 1), open = __ballot_sync(0xffffffffu, fl[m] & 2),
+                       carry = __ballot_sync(0xffffffffu, fl[m] & 4), last = __ballot_sync(0xffffffffu, fl[m] & 8),
+                       row = __ballot_sync(0xffffffffu, in_pool);
+        const uint32_t before = __shfl_up_sync(0xffffffffu, pos[m], 1);
+        const uint32_t turn = __ballot_sync(0xffffffffu, lane == 0 || pos[m] != before + 1);
+        if (lane == 0) {
+          meta[mb].taken[m0 + m] = taken;
+          meta[mb].open[m0 + m] = open;
+          meta[mb].carry[m0 + m] = carry;
+          meta[mb].last[m0 + m] = last;
+          meta[mb].row[m0 + m] = row;
+          meta[mb].turn[m0 + m] = turn;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&meta_full[mb]);
     }
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
-  } else if (warp == SEQ_WARP) {
-    // ======================= per-sequence results =======================
-    for (int b = blockIdx.x; b < a.c.B; b += gridDim.x) {
-      const AppendWin w = append_win(a, b, lane == 0);
-      if (lane == 0) {
-        a.t_out[b] = (int32_t)(w.t0 + w.n);
-        if (a.cache_len) a.cache_len[b] = w.t0 + w.n > 0 ? (int32_t)group_of(w.t0 + w.n, s) : 0;
+    if (warp == META_WARP1)                      // per-sequence results
+      for (int b = blockIdx.x; b < a.c.B; b += gridDim.x) {
+        const AppendWin w = append_win(a, b, lane == 0);
+        if (lane == 0) {
+          a.t_out[b] = (int32_t)(w.t0 + w.n);
+          if (a.cache_len) a.cache_len[b] = w.t0 + w.n > 0 ? (int32_t)group_of(w.t0 + w.n, s) : 0;
+        }
+        if (w.n == 0)
+          for (int k = lane; k < D; k += 32) a.tail_out[(int64_t)b * D + k] = a.tail_in[(int64_t)b * D + k];
       }
-      if (w.n == 0)
-        for (int k = lane; k < D; k += 32) a.tail_out[(int64_t)b * D + k] = a.tail_in[(int64_t)b * D + k];
-    }
   } else {
     // ======================= epilogue warps =======================
     const bool rope = ch >= R;                   // warp-uniform
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     {
-      // W^T as two bf16 parts into TMEM (loads issued at the kernel's start)
+      // -log2(e) W^T as two bf16 parts into TMEM (loads issued at the kernel's
+      // start): the accumulator and the bias are then the base-2 exponent's
       uint32_t hi[32], lo[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float w0 = wv[2 * k], w1 = wv[2 * k + 1];
+        const float w0 = wv[2 * k] * kNegLog2e, w1 = wv[2 * k + 1] * kNegLog2e;
         hi[k] = pack_bf16x2(w0, w1);
         const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[k]));
         lo[k] = pack_bf16x2(w0 - h.x, w1 - h.y);
@@ -346,143 +399,196 @@ __global__ void __launch_bounds__(NT, 1) paged_append_tc_kernel(const __grid_con
       tc_fence_before();
     }
     named_bar(1, 32 * (NEPI + 1));
-    const float bc = __ldg(a.m.b_c + ch);
+    const float bc = __ldg(a.m.b_c + ch) * kNegLog2e;
     const float* Pc = a.m.P + ch;
     const uint32_t sB = smem_u32(sm + OFF_B);
     // this channel's byte inside a swizzled 128-byte latent row (K block ch / 64)
     const uint32_t c_kb = (uint32_t)((ch & 255) >> 6), c_chunk = (uint32_t)((ch & 63) >> 3), c_in = (uint32_t)(ch & 7) * 2;
-    const int pair = (ch & 31) >> 1;
-    const double turn = rope ? turns[pair] : 0.0;
-    const float2 step = rope ? rope_cos_sin(1, turn) : make_float2(1.f, 0.f);
-    const float sgn = (ch & 1) ? 1.f : -1.f;     // odd channels: x1 cos + x0 sin; even: x0 cos - x1 sin
-    __nv_bfloat16* const state = reinterpret_cast<__nv_bfloat16*>(a.row_state) + (a.row_state ? ch : 0);
-    __nv_bfloat16* const pages = reinterpret_cast<__nv_bfloat16*>(a.p.pages) + ch;
-    uint32_t tc = 0;
-    bool queries = a.q_rope != nullptr;
-    for (int u = u_beg; u < u_end || queries; ++u, ++tc) {
-      if (queries) {
-        // this warp's share of the queries, at most 32 rows at a time: before
-        // the first tile, whose operands are still on their way
-        queries = false;
-        const int64_t warps = (int64_t)gridDim.x * NEPI;
-        int64_t rows = (a.c.N + warps - 1) / warps;
-        rows = rows < 32 ? (rows + 1) / 2 * 2 : 32;
-        for (int64_t k = ((int64_t)blockIdx.x * NEPI + part * 3 + q) * rows; k < a.c.N; k += warps * rows)
-          rotate_queries(a, k, (int)rows, turns);
-        if (u >= u_end) break;
+    uint32_t xo[8];                              // byte of the channel's 16-byte piece in row r of a swizzle atom
+#pragma unroll
+    for (int r = 0; r < 8; ++r) xo[r] = (c_chunk ^ (uint32_t)r) << 4;
+    // staged rows: [PCOL columns][32 channels] bf16, read back in 16-byte pieces
+    uint8_t* const ost = sm + OFF_OST + (part * 3 + q) * (PCOL * 64);
+    const uint32_t ost_ch = smem_u32(ost) + lane * 2;
+    const int ch0 = ct * NCT + q * 32;           // the warp's first channel
+    const uint64_t turn = turns[lane >> 1];      // (rope quarter) the channel's pair
+    const float2 step = rope_cos_sin(1, turn);
+    auto turned = [&](uint32_t pair, float2 cs) -> float {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pair));
+      return ch & 1 ? f.y * cs.x + f.x * cs.y : f.x * cs.x - f.y * cs.y;
+    };
+    // P of a tile's columns [p0, p0 + PCOL), this warp's channels, into its
+    // block of shared memory by asynchronous copies: issued while the tile
+    // before is stored (a copy a column: the same row again is an L1 hit)
+    const int p0 = PCOL * part;
+    const uint32_t pbuf = smem_u32(sm + OFF_P + (size_t)(part * 3 + q) * (PCOL * 128)) + lane * 4;
+    auto fetch = [&](const Meta& mt) {
+#pragma unroll 2
+      for (int k = 0; k < PCOL; k += 4) {
+        const int4 r = *reinterpret_cast<const int4*>(&mt.prow[p0 + k]);
+        const int rows[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(pbuf + (k + e) * 128), "l"(Pc + (int64_t)rows[e] * D)
+                       : "memory");
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    ok = warp_wait(&meta_full[0], 0);
+    if (ok) fetch(meta[0]);
+    uint32_t tc = 0;
+    for (int u = u_beg; u < u_end && ok; ++u, ++tc) {
       const int ab = tc & 1, sb = ab * KB;
       const uint32_t par = (tc >> 1) & 1;
       const int64_t base = (int64_t)u * nout - halo;
-      if (!warp_wait(&meta_full[ab], par)) { ok = false; break; }
       const Meta& mt = meta[ab];
-      const int cb = 32 * part > halo ? 32 * part : halo, ce = 32 * part + 32;
+      // this warp's columns [cb, ce) of [p0, p0 + PCOL); masks are bits of the column in its word of 32
+      const int cb = p0 > halo ? p0 : halo;
       const int64_t lastc = a.c.N - base;        // columns past it are no token rows
-      const int hi_c = ce < lastc ? ce : (int)lastc;
-      const int back = cb < hi_c ? mt.tok[cb].w >> F_BACK : 0;
-      float run = 0.f;
-      float2 cs = make_float2(1.f, 0.f);
-      int cs_pos = -2, cs_seq = -1, cs_age = 0;  // position and sequence that cs holds
-      // chunk loads: P and, where a sequence goes on in an open group, its tail
-      float pn[16], tn[16];
-      auto fetch = [&](int c0) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int4 t = mt.tok[c0 + k];
-          pn[k] = __ldg(Pc + (int64_t)t.x * D);
-          tn[k] = 0.f;
-          if (t.w & F_CARRY) tn[k] = a.tail_in[(int64_t)mt.seq[c0 + k] * D + ch];
+      const int ce = p0 + PCOL < lastc ? p0 + PCOL : (int)lastc;
+      if (cb < ce) {
+        const uint32_t vrow = rope ? smem_u32(sm + OFF_KR + ab * KRBLK) + (uint32_t)(lane >> 1) * 4 : sB + (sb + c_kb) * BBLK + c_in;
+        // Columns before cb belong to a group that began before them: it is
+        // summed again from its start in the chunk.  A few of them singly (same
+        // P, and the tail if that start is the chunk's), more in chunks of 16.
+        const int back = mt.back[cb], c1 = cb - back;
+        const bool single = back > 0 && back < 8 && cb == p0;
+        const int c_beg = single ? p0 : c1 & ~15;
+        float ph = 0.f, run = 0.f;
+        if (single) {
+          ph = __ldg(Pc + (int64_t)mt.prow[cb] * D);
+          if (mt.carry[c1 >> 5] >> (c1 & 31) & 1) run = a.tail_in[(int64_t)mt.seq[cb] * D + ch];
         }
-      };
-      // the key entry of a column: the rotated pair, fp32
-      auto key = [&](int col, const int4& t) -> float {
-        const uint32_t row = smem_u32(sm + OFF_KR + ab * KRBLK) + (uint32_t)col * (DR * 2) + (uint32_t)(ch & 31) * 2;
-        uint16_t own, other;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(own) : "r"(row));
-        if (!a.rotate) return __bfloat162float(__ushort_as_bfloat16(own));
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(other) : "r"(row ^ 2u));
-        const int sq = mt.seq[col];
-        if (sq != cs_seq || t.z != cs_pos + 1 || cs_age == 7) {
-          cs = rope_cos_sin(t.z, turn);
-          cs_age = 0;
-        } else {
-          cs = make_float2(cs.x * step.x - cs.y * step.y, cs.x * step.y + cs.y * step.x);
-          ++cs_age;
-        }
-        cs_pos = t.z;
-        cs_seq = sq;
-        return __bfloat162float(__ushort_as_bfloat16(own)) * cs.x + sgn * __bfloat162float(__ushort_as_bfloat16(other)) * cs.y;
-      };
-      auto latent = [&](int col) -> float {
-        uint16_t raw;
-        const uint32_t at = sB + (sb + c_kb) * BBLK + (uint32_t)(col >> 3) * 1024 + (uint32_t)(col & 7) * 128 +
-                            ((c_chunk ^ (uint32_t)(col & 7)) << 4) + c_in;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at));
-        return __bfloat162float(__ushort_as_bfloat16(raw));
-      };
-      if (cb < hi_c) fetch(cb & ~15);
-      ok = warp_wait(&acc_full[ab], par) && warp_wait(&k_full[sb], par) && warp_wait(&k_full[sb + c_kb], par);
-      tc_fence_after();
-      if (!ok) break;
-      // the first group's earlier tokens, summed again from its start
-      for (int col = cb - back; col < cb && cb < hi_c; ++col) {
-        const int4 t = mt.tok[col];
-        const float g = __uint_as_float(tmem_ld1(lane_base + ab * ACC_STRIDE + col));
-        const float pa = __ldg(Pc + (int64_t)t.x * D) * kNegLog2e;
-        const float x = rope ? key(col, t) : latent(col);
-        float start = run;
-        if (t.w & F_OPEN) start = t.w & F_CARRY ? a.tail_in[(int64_t)mt.seq[col] * D + ch] : 0.f;
-        tmem_wait_ld();
-        run = start + gated(x, fmaf(g, pa, bc * pa));
-      }
-      for (int c0 = cb & ~15; c0 < hi_c; c0 += 16) {
-        uint32_t g[16];
-        tmem_ld16(lane_base + ab * ACC_STRIDE + c0, g);
-        float v[16], pc[16], tl[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          pc[k] = pn[k];
-          tl[k] = tn[k];
-        }
-        if (c0 + 16 < hi_c) fetch(c0 + 16);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (rope) {
-            v[k] = 0.f;
-            if (c0 + k >= cb && c0 + k < hi_c) v[k] = key(c0 + k, mt.tok[c0 + k]);
-          } else {
-            v[k] = latent(c0 + k);
+        ok = warp_wait(&acc_full[ab], par) && warp_wait(&k_full[sb], par) && warp_wait(&k_full[sb + c_kb], par);
+        tc_fence_after();
+        if (!ok) break;
+        const uint32_t acc = lane_base + ab * ACC_STRIDE;
+        if (single) {
+#pragma unroll 1
+          for (int col = c1; col < cb; ++col) {
+            const uint32_t g = tmem_ld1(acc + col);
+            float x;
+            if (rope) {
+              uint32_t pair;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair) : "r"(vrow + (uint32_t)col * (DR * 2)));
+              x = turned(pair, rope_cos_sin(mt.pos[col], turn));
+            } else {
+              uint16_t raw;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(vrow + (uint32_t)(col >> 3) * 1024 + (uint32_t)(col & 7) * 128 +
+                                                                       ((c_chunk ^ (uint32_t)(col & 7)) << 4)));
+              x = __bfloat162float(__ushort_as_bfloat16(raw));
+            }
+            tmem_wait_ld();
+            run += gated(x, (__uint_as_float(g) + bc) * ph);
           }
         }
-        tmem_wait_ld();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+        for (int c0 = c_beg; c0 < ce; c0 += 16) {
+          uint32_t g[16];
+          tmem_ld16(acc + c0, g);
+          const int word = c0 >> 5, bit = c0 & 31;
+          float v[16], pc[16];
+          if (c0 >= p0) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float pa = pc[k] * kNegLog2e;
-          v[k] = gated(v[k], fmaf(__uint_as_float(g[k]), pa, bc * pa));
-        }
+            for (int k = 0; k < 16; ++k) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(pc[k]) : "r"(pbuf + (c0 - p0 + k) * 128));
+          } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int col = c0 + k;
-          if (col >= cb && col < hi_c) {
-            const int4 t = mt.tok[col];
-            run = (t.w & F_OPEN ? tl[k] : run) + v[k];
-            if (t.w & F_TAKEN) {
-              const __nv_bfloat16 o = __float2bfloat16_rn(run);
-              if (a.row_state) state[(base + col) * D] = o;
-              if (t.y >= 0) pages[(int64_t)t.y * a.p.row_stride] = o;
-              if (t.w & F_LAST) a.tail_out[(int64_t)mt.seq[col] * D + ch] = run;
+            for (int k = 0; k < 16; ++k) pc[k] = __ldg(Pc + (int64_t)mt.prow[c0 + k] * D);
+          }
+          if (rope) {
+            const uint32_t at = vrow + (uint32_t)c0 * (DR * 2);
+            uint32_t pair[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[k]) : "r"(at + k * (DR * 2)));
+            if ((mt.turn[word] >> bit & 0xfffeu) == 0) {  // one run of positions
+              const uint32_t first = mt.pos[c0];
+              float2 cs = make_float2(1.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                cs = (k & 7) == 0 ? rope_cos_sin(first + k, turn)
+                                  : make_float2(cs.x * step.x - cs.y * step.y, cs.x * step.y + cs.y * step.x);
+                v[k] = turned(pair[k], cs);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = turned(pair[k], rope_cos_sin(mt.pos[c0 + k], turn));
+            }
+          } else {
+            const uint32_t at = vrow + (uint32_t)(c0 >> 3) * 1024;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              uint16_t raw;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at + (k >> 3) * 1024 + (k & 7) * 128 + xo[k & 7]));
+              v[k] = __bfloat162float(__ushort_as_bfloat16(raw));
+            }
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = gated(v[k], (__uint_as_float(g[k]) + bc) * pc[k]);
+          // the sums, in token order (what a column before the first open group
+          // holds is never stored); a chunk that goes on in an open group starts
+          // at its tail
+          const uint32_t open = mt.open[word] >> bit, carry = mt.carry[word] >> bit & 0xffffu;
+          if (carry) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (carry >> k & 1) v[k] += a.tail_in[(int64_t)mt.seq[c0 + k] * D + ch];
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            run = (open >> k & 1 ? 0.f : run) + v[k];
+            v[k] = run;
+          }
+          if (c0 >= p0) {
+            const uint32_t last = mt.last[word] >> bit & 0xffffu;
+            if (last) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if ((last >> k & 1) && c0 + k >= cb && c0 + k < ce) a.tail_out[(int64_t)mt.seq[c0 + k] * D + ch] = v[k];
+            }
+            const uint32_t at = ost_ch + (uint32_t)(c0 - p0) * 64;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const uint32_t w = pack_bf16x2(v[k], v[k + 1]);
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + k * 64), "h"((uint16_t)(w & 0xffffu)) : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + k * 64 + 64), "h"((uint16_t)(w >> 16)) : "memory");
             }
           }
         }
+        if (u + 1 < u_end) {
+          if (!warp_wait(&meta_full[ab ^ 1], ((tc + 1) >> 1) & 1)) { ok = false; break; }
+          fetch(meta[ab ^ 1]);
+        }
+        // the staged rows, 16 bytes of eight rows a step
+        __syncwarp();
+        const uint32_t taken = a.row_state ? mt.taken[p0 >> 5] : 0u, rows = mt.row[p0 >> 5];
+        const int piece = lane & 3;
+#pragma unroll
+        for (int k8 = 0; k8 < PCOL / 8; ++k8) {
+          const int r = 8 * k8 + (lane >> 2), col = p0 + r, bit = col & 31;
+          const uint4 w = *reinterpret_cast<const uint4*>(ost + r * 64 + piece * 16);
+          if (col >= cb && col < ce) {
+            if (taken >> bit & 1)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.row_state) + (base + col) * D + ch0 + piece * 8) = w;
+            if (rows >> bit & 1)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.p.pages) + (int64_t)mt.pool[col] * a.p.row_stride +
+                                        ch0 + piece * 8) = w;
+          }
+        }
+      } else if (u + 1 < u_end) {
+        if (!warp_wait(&meta_full[ab ^ 1], ((tc + 1) >> 1) & 1)) { ok = false; break; }
+        fetch(meta[ab ^ 1]);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&acc_empty[ab]);
         mbar_arrive(&meta_empty[ab]);
-        for (int kb = 0; kb < KB; ++kb) mbar_arrive(&k_empty[sb + kb]);
+        mbar_arrive(&k_empty[ab]);
       }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy may still be writing shared memory at exit
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
   }
 
@@ -504,6 +610,13 @@ cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMa
   if (dev >= 64 || !(done_mask & (1ull << dev))) {
     e = cudaFuncSetAttribute(ptp::paged_append_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ptp::SMEM);
     if (e != cudaSuccess) return e;
+    // the same shared-memory configuration for both kernels: they share SMs
+    e = cudaFuncSetAttribute(ptp::paged_append_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(ptp::paged_rotate_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     if (dev < 64) done_mask |= 1ull << dev;
   }
   const int n_tiles = (int)cdiv(a.c.N, ptp::NTOK - (a.s - 1));
@@ -519,7 +632,12 @@ cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMa
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ptp::paged_append_tc_kernel, m, a, n_tiles);
+  e = cudaLaunchKernelEx(&cfg, ptp::paged_append_tc_kernel, m, a, n_tiles);
+  if (e != cudaSuccess || !a.q_rope) return e;
+  cfg.gridDim = dim3((unsigned)cdiv(a.c.N, ptp::QT / 32 * ptp::QROWS));
+  cfg.blockDim = dim3(ptp::QT);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, ptp::paged_rotate_kernel, a);
 }
 
 }  // namespace mtla

@@ -350,12 +350,28 @@ static auto simt_kernel(int r) -> void (*)(const PagedAttnArgs) {
 }  // namespace psimt
 
 int paged_simt_grid(int r, int d_R, int dtype, int sms) {
+  // the occupancy of the last widths asked for on this thread (the widest
+  // shared memory is allowed once per kernel and device)
+  struct Last {
+    int dev = -1, r, d_R, dtype, grid;
+  };
+  thread_local Last last;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (last.dev == dev && last.r == r && last.d_R == d_R && last.dtype == dtype) return last.grid;
   auto k = dtype == MTLA_BF16 ? psimt::simt_kernel<__nv_bfloat16>(r) : psimt::simt_kernel<float>(r);
-  const size_t smem = psimt::smem_bytes(r + d_R);
   int occ = 0;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, smem) != cudaSuccess || occ < 1) return 0;
-  return sms * (occ < 4 ? occ : 4);
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psimt::smem_bytes(576)) != cudaSuccess)
+    return 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, psimt::smem_bytes(r + d_R)) != cudaSuccess ||
+      occ < 1)
+    return 0;
+  last.dev = dev;
+  last.r = r;
+  last.d_R = d_R;
+  last.dtype = dtype;
+  last.grid = sms * (occ < 4 ? occ : 4);
+  return last.grid;
 }
 
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st) {

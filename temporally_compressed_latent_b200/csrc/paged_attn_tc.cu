@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       // pool row of this lane's group (past the pool: the box is filled with zeros)
       auto group_row = [&](int g) -> int32_t {
         if (g >= R8g) return 0;
-        const int k = (int)((uint32_t)(g * 8) / (uint32_t)a.p.page_rows);
+        const int k = (int)div32((uint32_t)(g * 8), a.p.div_rows);
         const int32_t page = __ldg(a.p.table + (int64_t)it.b * a.p.table_pages + k);
         if (page < 0 || page >= a.p.num_pages) {
           set_err(a.dev_err, MTLA_DEVERR_CAPACITY);

@@ -10,13 +10,15 @@
 // A cluster of CL blocks takes a sequence: only one row of p and of q is read
 // (the drafts' probabilities are gathers), so the vocabulary is split over the
 // cluster for its latency and bandwidth, and the blocks exchange their sums
-// through distributed shared memory.  A warp sums 1024 entries at a time and
-// notes each sum; after the exchange the one block that holds the drawn index
-// reads one such run again and scans it.  Sums are in double precision: the
-// running sum over 10^5 entries of size 10^-5 must place the border between
-// neighbours, which 24 bits would miss once in a hundred draws.  Bound by the
-// two rows' HBM reads (large batches) or by the chain of four dependent reads
-// (small ones).
+// through distributed shared memory.  A warp sums 256 entries at a time, eight
+// a lane, and notes each sum; after the exchange the one block that holds the
+// drawn index scans its sums and reads one such run again.  Sums are in double
+// precision: the running sum over 10^5 entries of size 10^-5 must place the
+// border between neighbours, which 24 bits would miss once in a hundred draws.
+// They are trees of depth three in a lane and five across it (an addition in
+// double takes tens of cycles: a chain of 32 cost 2 us a step here).
+// Bound by the two rows' HBM reads (large batches) or by the chain of four
+// dependent reads and the cluster's barriers (small ones).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -26,19 +28,75 @@ namespace vfy {
 
 namespace cg = cooperative_groups;
 constexpr int CL = 8;
-constexpr int NT = 256, NW = NT / 32;
-constexpr int RUN = 1024;                           // entries a warp sums at a time
-constexpr int MAXV = 1 << 24;
+constexpr int NT = 512, NW = NT / 32;
+constexpr int RUN = 256;                            // entries a warp sums at a time
+constexpr int MAXV = 1 << 22;
 constexpr int MAXRUNS = MAXV / RUN / CL;            // runs of a block: 2048
 
 // entries that are NaN, infinite or not above zero count as zero
 __device__ __forceinline__ float clean(float x) { return x > 0.f && x <= 3.4028234663852886e38f ? x : 0.f; }
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ double warp_scan(double x) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
 
+// What the next token is drawn from.
+struct Weights {
+  const float *p, *q;   // q: null where p alone counts
+  int V, hole;          // hole: an index without weight, or -1
+  // eight entries of a run starting at v0: lane l's are v0 + 4 l .. + 3 and v0 +
+  // 128 + 4 l .. + 3 (in index order a lane holds two quadruples)
+  template <bool VEC>
+  __device__ __forceinline__ void load(int v0, float (&a)[8], float (&b)[8]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int v = v0 + 128 * h + 4 * lane;
+      if (VEC && v + 4 <= V) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p + v));
+        a[4 * h] = x.x; a[4 * h + 1] = x.y; a[4 * h + 2] = x.z; a[4 * h + 3] = x.w;
+        if (q) {
+          const float4 y = __ldg(reinterpret_cast<const float4*>(q + v));
+          b[4 * h] = y.x; b[4 * h + 1] = y.y; b[4 * h + 2] = y.z; b[4 * h + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[4 * h + e] = v + e < V ? __ldg(p + v + e) : 0.f;
+          if (q) b[4 * h + e] = v + e < V ? __ldg(q + v + e) : 0.f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void weigh(int v0, const float (&a)[8], const float (&b)[8], double (&w)[8]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = clean(a[k]), y = q ? clean(b[k]) : 0.f;
+      // (a float difference has the sign of the exact one)
+      w[k] = x > y ? (double)x - (double)y : 0.0;
+      if (v0 + 128 * (k >> 2) + 4 * lane + (k & 3) == hole) w[k] = 0.0;
+    }
+  }
+};
+
+template <bool VEC>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ double run_sum[MAXRUNS];
-  __shared__ double my_total, all[CL];
-  __shared__ int first_drop, pick;
+  __shared__ double warp_total[NW];
+  __shared__ double totals[2][CL];                  // every block's sum, written by the blocks themselves
+  __shared__ int first_drop;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster.block_rank(), b = blockIdx.x / CL;
 
@@ -52,6 +110,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
     }
     return;
   }
+  // (the blocks of the cluster have all started when the first sum is sent)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const float u = a.u_sample[b];
   // ---- the first draft dropped (n - 1: none); every block finds it for itself
   if (tid == 0) first_drop = n - 1;
   __syncthreads();
@@ -60,10 +121,11 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
     if (i < n - 1) {
       const int64_t row = first + i;
       const int x = a.tokens[row + 1];
+      const float ua = a.u_accept[row];
       bool keep = false;
       if (x >= 0 && x < a.V) {
         const double p = clean(a.p[row * a.ld_p + x]), q = a.q ? clean(a.q[row * a.ld_q + x]) : 1.f;
-        keep = (double)a.u_accept[row] * q < p;
+        keep = (double)ua * q < p;
       } else if (rank == 0) {
         set_err(a.dev_err, MTLA_DEVERR_TOKEN);
       }
@@ -73,52 +135,52 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
     if (first_drop < i0 + NT) break;
   }
   const int drop = first_drop;
-  const float* pr = a.p + (int64_t)(first + drop) * a.ld_p;
-  const float* qr = a.q ? a.q + (int64_t)(first + drop) * a.ld_q : nullptr;
+  const bool dropped = drop < n - 1;
+  Weights w;
+  w.p = a.p + (int64_t)(first + drop) * a.ld_p;
+  w.q = a.q && dropped ? a.q + (int64_t)(first + drop) * a.ld_q : nullptr;
+  w.V = a.V;
   // certain drafts (no q): the residual is p without the dropped token
-  const int hole = !a.q && drop < n - 1 ? a.tokens[first + drop + 1] : -1;
-  bool residual = drop < n - 1;
+  w.hole = !a.q && dropped ? a.tokens[first + drop + 1] : -1;
 
   const int runs = (a.V + RUN - 1) / RUN, per = (runs + CL - 1) / CL;
   const int r_beg = rank * per < runs ? rank * per : runs, r_end = r_beg + per < runs ? r_beg + per : runs;
-  auto weight = [&](int v) -> double {
-    const double p = clean(pr[v]);
-    if (!residual) return p;
-    if (qr) {
-      const double d = p - (double)clean(qr[v]);
-      return d > 0.0 ? d : 0.0;
-    }
-    return v == hole ? 0.0 : p;
-  };
+  const int mine = r_end - r_beg;
   double total = 0.0;
-  for (;;) {
-    for (int r = r_beg + warp; r < r_end; r += NW) {
-      double sum = 0.0;
-      const int v0 = r * RUN + lane;
-#pragma unroll 8
-      for (int k = 0; k < RUN / 32; ++k) {
-        const int v = v0 + 32 * k;
-        if (v < a.V) sum += weight(v);
-      }
+  int round = 0;
+  for (;; ++round) {
+    double sum = 0.0;
+    // two runs at a time: up to 32 loads of a lane in flight
+    for (int r = warp; r < mine; r += 2 * NW) {
+      float pa[2][8], qa[2][8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) run_sum[r - r_beg] = sum;
+      for (int h = 0; h < 2; ++h)
+        if (r + h * NW < mine) w.load<VEC>((r_beg + r + h * NW) * RUN, pa[h], qa[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (r + h * NW < mine) {
+          double x[8];
+          w.weigh((r_beg + r + h * NW) * RUN, pa[h], qa[h], x);
+          const double s = warp_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+          if (lane == 0) run_sum[r + h * NW] = s;
+          sum += s;
+        }
     }
+    if (lane == 0) warp_total[warp] = sum;
+    if (round == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
     if (warp == 0) {
-      double sum = 0.0;
-      for (int r = lane; r < r_end - r_beg; r += 32) sum += run_sum[r];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) my_total = sum;
+      const double s = warp_sum(lane < NW ? warp_total[lane] : 0.0);
+      // to every block of the cluster (two buffers: a second round's sums do
+      // not meet late readers of the first's)
+      if (lane < CL) *cluster.map_shared_rank(&totals[round & 1][rank], lane) = s;
     }
     cluster.sync();
-    if (tid < CL) all[tid] = *cluster.map_shared_rank(&my_total, tid);
-    cluster.sync();  // every block has read the totals: they may be written again, and blocks may leave
     total = 0.0;
-    for (int r = 0; r < CL; ++r) total += all[r];
-    if (total > 0.0 || !residual) break;
-    residual = false;  // nothing above q: draw from p
+    for (int r = 0; r < CL; ++r) total += totals[round & 1][r];
+    if (total > 0.0 || !dropped || round > 0) break;
+    w.q = nullptr;  // nothing above q: draw from p
+    w.hole = -1;
   }
   if (rank == 0 && tid == 0) a.n_keep[b] = drop + 1;
   if (!(total > 0.0)) {
@@ -129,71 +191,82 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
     return;
   }
   // ---- the block, the run and the entry where the running sum passes the target
-  const float u = a.u_sample[b];
   const double target = (u > 0.f ? (double)u : 0.0) * total;
   int owner = -1;
   double before = 0.0;
   {
     double c = 0.0;
     for (int r = 0; r < CL; ++r) {
-      if (all[r] > 0.0) {
+      const double t = totals[round & 1][r];
+      if (t > 0.0) {
         // (the last block with any weight takes what rounding leaves over)
         owner = r;
         before = c;
-        if (c + all[r] > target) break;
+        if (c + t > target) break;
       }
-      c += all[r];
+      c += t;
     }
   }
-  if (owner != rank) return;
-  if (tid == 0) {
-    double c = before;
-    int at = -1;
-    for (int r = 0; r < r_end - r_beg; ++r) {
-      if (run_sum[r] > 0.0) {
-        at = r;
-        before = c;
-        if (c + run_sum[r] > target) break;
-      }
-      c += run_sum[r];
+  if (owner != rank || warp != 0) return;
+  // warp 0 scans the sums of the block's runs, 32 at a time; the last run with
+  // any weight takes what rounding leaves over
+  int pick = -1;
+  double at = before, c = before;
+  for (int r0 = 0; r0 < mine; r0 += 32) {
+    const double x = r0 + lane < mine ? run_sum[r0 + lane] : 0.0;
+    const double pre = warp_scan(x);
+    const uint32_t some = __ballot_sync(0xffffffffu, x > 0.0);
+    const uint32_t hits = __ballot_sync(0xffffffffu, x > 0.0 && c + pre > target);
+    if (some) {
+      const int l = hits ? __ffs(hits) - 1 : 31 - __clz(some);
+      pick = r0 + l;
+      at = c + __shfl_sync(0xffffffffu, pre - x, l);
     }
-    pick = at;
-    my_total = before;
+    if (hits) break;
+    c += __shfl_sync(0xffffffffu, pre, 31);
   }
-  __syncthreads();
-  if (warp != 0) return;
-  // warp 0 scans the run: lane l holds entries 32 l .. 32 l + 31
-  const int v0 = (r_beg + pick) * RUN + 32 * lane;
-  before = my_total;
-  double w[32], sum = 0.0;
+  // and that run's entries, in index order: the lanes' first quadruples, then
+  // their second
+  const int v0 = (r_beg + pick) * RUN;
+  float pa[8], qa[8];
+  double x[8];
+  w.load<VEC>(v0, pa, qa);
+  w.weigh(v0, pa, qa, x);
+  c = at;
+  int token = -1;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    w[k] = v0 + k < a.V ? weight(v0 + k) : 0.0;
-    sum += w[k];
-  }
-  double pre = sum;
+  for (int h = 0; h < 2; ++h) {
+    const double s01 = x[4 * h] + x[4 * h + 1], s = s01 + (x[4 * h + 2] + x[4 * h + 3]);
+    const double pre = warp_scan(s), base = c + (pre - s);
+    const double run[4] = {base + x[4 * h], base + s01, base + (s01 + x[4 * h + 2]), base + s};
+    int hit = -1, lastp = -1;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double v = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += v;
-  }
-  double c = before + (pre - sum);
-  int hit = -1, lastp = -1;
+    for (int k = 3; k >= 0; --k)
+      if (x[4 * h + k] > 0.0 && run[k] > target) hit = v0 + 128 * h + 4 * lane + k;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    c += w[k];
-    if (w[k] > 0.0) lastp = v0 + k;
-    if (hit < 0 && c > target && w[k] > 0.0) hit = v0 + k;
+    for (int k = 0; k < 4; ++k)
+      if (x[4 * h + k] > 0.0) lastp = v0 + 128 * h + 4 * lane + k;
+    const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0), some = __ballot_sync(0xffffffffu, lastp >= 0);
+    if (hits) {
+      token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
+      break;
+    }
+    // no entry passes (rounding): the last one with weight
+    if (some) token = __shfl_sync(0xffffffffu, lastp, 31 - __clz(some));
+    c += __shfl_sync(0xffffffffu, pre, 31);
   }
-  const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0), some = __ballot_sync(0xffffffffu, lastp >= 0);
-  // no entry passes (rounding): the last one with weight
-  if (hits ? lane == __ffs(hits) - 1 : lane == 31 - __clz(some)) a.next_token[b] = hits ? hit : lastp;
+  if (lane == 0) a.next_token[b] = token;
 }
 
 }  // namespace vfy
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  vfy::verify_kernel<<<(unsigned)a.B * vfy::CL, vfy::NT, 0, st>>>(a);
+  // rows that all start on 16 bytes are read four entries at a time
+  const bool vec = (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && a.ld_p % 4 == 0 &&
+                   (!a.q || ((reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.ld_q % 4 == 0));
+  const unsigned grid = (unsigned)a.B * vfy::CL;
+  if (vec) vfy::verify_kernel<true><<<grid, vfy::NT, 0, st>>>(a);
+  else vfy::verify_kernel<false><<<grid, vfy::NT, 0, st>>>(a);
   return cudaGetLastError();
 }
 

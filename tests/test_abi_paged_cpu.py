@@ -99,7 +99,7 @@ def test_verify_refusals():
     def call(B=1, N=3, V=10, p=P, ldp=10, q=P, ldq=10, tok=P, start=P, ua=P, us=P, keep=P, nxt=P, err=P):
         return mtla.lib.mtla_verify_drafts(B, N, V, p, ldp, q, ldq, tok, start, ua, us, keep, nxt, err, None)
 
-    assert call(B=-1) == INVALID and call(N=-1) == INVALID and call(V=0) == INVALID and call(V=(1 << 24) + 1) == INVALID
+    assert call(B=-1) == INVALID and call(N=-1) == INVALID and call(V=0) == INVALID and call(V=(1 << 22) + 1) == INVALID
     assert call(ldp=9) == INVALID and call(ldq=9) == INVALID
     for name in ("p", "tok", "start", "ua", "us", "keep", "nxt", "err"):
         assert call(**{name: None}) == INVALID
