@@ -132,14 +132,16 @@ __device__ __forceinline__ float2 rope_cos_sin(uint32_t pos, uint64_t turns) {
 // blocks) or a long prompt (a block takes many items).  Where a cut falls
 // inside an item its parts are combined by a second kernel.
 //
-// kt = ceil((8 ceil(R/8) + 8 g) / (8 q)) with g = ceil(tokens / 8); nested
-// floors of nested divisions fold into one,
+// kt = ceil((ceil(R/8) + g) / q) with g = ceil(tokens / 8) and R = floor((t - 1)
+// / s): nested divisions fold into one,
 //   kt = floor((t + 7 s - 1 + 8 s (g + q - 1)) / (8 q s)),
 // linear in t, so the sum over a sequence's items is a sum of floors of a
 // linear function, which has a logarithmic-time form (floor_sum).
 // ----------------------------------------------------------------------------
 struct PlanArgs {
   int s, tpt, q, item_cost;
+  int min_share;   // least weight worth a block of its own
+  FastDiv div_s;
 };
 // sum over i in [0, n) of floor((a i + b) / m), by the Euclidean recursion
 __device__ inline int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
@@ -163,10 +165,12 @@ __device__ inline int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t
   }
   return (int64_t)ans;
 }
-// key tiles of an item whose last token has time t and which holds k tokens
-__device__ __forceinline__ int64_t item_tiles(const PlanArgs& a, int64_t t, int k) {
-  const int g = (k + 7) >> 3;
-  return (t + 7ll * a.s - 1 + 8ll * a.s * (g + a.q - 1)) / (8ll * a.q * a.s);
+// cache rows below the query of time t: R = ceil(t / s) - 1 (1 <= t < 2^32)
+__device__ __forceinline__ int rows_below(const PlanArgs& a, int64_t t) { return (int)div32((uint32_t)(t - 1), a.div_s); }
+// key tiles of an item whose last token has time t and which holds k tokens (q
+// is 4 or 8)
+__device__ __forceinline__ int item_tiles(const PlanArgs& a, int64_t t, int k) {
+  return (((rows_below(a, t) + 7) >> 3) + ((k + 7) >> 3) + a.q - 1) >> (a.q == 8 ? 3 : 2);
 }
 // weight of a sequence's first m items (chunk of n tokens after t0)
 __device__ inline int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int64_t m) {
@@ -191,20 +195,35 @@ struct Item {
   int slot;         // partial-result slot, or -1: the whole item is here, its results go out directly
 };
 
+// Blocks that get a share: no more than give each min_share of the weight C.
+__device__ __forceinline__ int64_t share_blocks(const PlanArgs& a, int64_t C, int grid) {
+  if (C >= (int64_t)a.min_share * grid) return grid;
+  return ((int)C + a.min_share - 1) / a.min_share;
+}
 // Shares: block x of G takes [C x / G, C (x + 1) / G).
-__device__ __forceinline__ int64_t share_lo(int64_t C, int64_t G, int64_t x) { return C * x / G; }
+__device__ __forceinline__ int64_t share_lo(int64_t C, int64_t G, int64_t x) {
+  // (a 64-bit division is a few hundred cycles of one warp's time)
+  if (C < (1 << 20)) return (uint32_t)C * (uint32_t)x / (uint32_t)G;  // G < 2^12
+  return C * x / G;
+}
 
+// With no more sequences than threads the plan keeps every sequence's window in
+// shared memory for the walk.
+constexpr int PLAN_WINS = 512;
 struct PlanShared {
   int64_t warp_sum[32];
-  int64_t C, before;  // total weight; weight of the sequences before `b`
-  int b;              // sequence holding this block's first position
+  int64_t C, G, before;  // total weight; blocks with a share; weight of the sequences before `b`
+  int b;                 // sequence holding this block's first position
+  int kept;              // windows in win
+  int most;              // most tokens of an item
 };
 
 // The chunk window the attention takes (a sequence whose rows exceed its table,
 // or with a negative time, takes none).
-__device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p, int s, int b, int32_t* dev_err) {
+__device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p, const FastDiv& div_s, int b,
+                                           int32_t* dev_err) {
   SeqWin w = seq_win(c, b);
-  if (w.n > 0 && (w.t0 < 0 || group_of(w.t0 + w.n, s) - 1 > table_rows(p))) {
+  if (w.n > 0 && (w.t0 < 0 || (int64_t)div32((uint32_t)(w.t0 + w.n - 1), div_s) > table_rows(p))) {
     if (dev_err) set_err(dev_err, MTLA_DEVERR_CAPACITY);
     w.n = 0;
   }
@@ -214,18 +233,24 @@ __device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p,
 // Taken by every thread of the block: the total weight C, and the sequence
 // that holds position share_lo(C, G, x).  One pass over the sequences (each
 // thread sums a run of them) and one block scan; the thread whose run holds
-// the position walks its run again.  x < 0: only C.
+// the position walks its run again.  win: PLAN_WINS windows, kept where every
+// thread has one sequence at most.
 template <int NT>
 __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int grid, int x,
-                                  int32_t* dev_err, PlanShared* sh) {
+                                  int32_t* dev_err, PlanShared* sh, SeqWin* win) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (c.B + NT - 1) / NT;
   const int b0 = tid * per < c.B ? tid * per : c.B, b1 = b0 + per < c.B ? b0 + per : c.B;
   int64_t sum = 0;
+  int most = 0;
+  if (tid == 0) sh->most = 0;
   for (int b = b0; b < b1; ++b) {
-    const SeqWin w = attn_win(c, p, a.s, b, x == 0 ? dev_err : nullptr);
+    const SeqWin w = attn_win(c, p, a.div_s, b, x == 0 ? dev_err : nullptr);
     sum += items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
+    most = most > w.n ? most : w.n;
+    if (per == 1) win[b] = w;
   }
+  most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(most < a.tpt ? most : a.tpt));
   int64_t pre = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -235,20 +260,25 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
   if (lane == 31) sh->warp_sum[warp] = pre;
   if (tid == 0) sh->b = -1;
   __syncthreads();
+  if (lane == 0) atomicMax(&sh->most, most);
   int64_t base = 0, C = 0;
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) base += sh->warp_sum[w];
     C += sh->warp_sum[w];
   }
-  if (tid == 0) sh->C = C;
-  const int64_t G = C < grid ? C : grid;
-  if (x >= 0 && x < G) {
+  const int64_t G = share_blocks(a, C, grid);
+  if (tid == 0) {
+    sh->C = C;
+    sh->G = G;
+    sh->kept = per == 1;
+  }
+  if (x < G) {
     const int64_t lo = share_lo(C, G, x);
     int64_t at = base + pre - sum;
     if (lo >= at && lo < at + sum) {
       int b = b0;
-      for (; b + 1 < b1; ++b) {
-        const SeqWin w = attn_win(c, p, a.s, b, nullptr);
+      for (; b + 1 < b1; ++b) {  // (not taken where every thread has one)
+        const SeqWin w = attn_win(c, p, a.div_s, b, nullptr);
         const int64_t k = items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
         if (lo < at + k) break;
         at += k;
@@ -269,6 +299,7 @@ struct ItemWalk {
   int batch;              // first sequence of the window batch in the lanes
   int w_first, w_n;       // this lane's sequence batch + lane
   int64_t w_t0;
+  const SeqWin* win;      // the plan's windows, or null
 
   __device__ __forceinline__ void load(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int b0) {
     batch = b0;
@@ -277,17 +308,18 @@ struct ItemWalk {
     w.first = 0;
     w.n = 0;
     w.t0 = 0;
-    if (bb < c.B) w = attn_win(c, p, a.s, bb, nullptr);
+    if (bb < c.B) w = win ? win[bb] : attn_win(c, p, a.div_s, bb, nullptr);
     w_first = w.first;
     w_n = w.n;
     w_t0 = w.t0;
   }
 
-  __device__ inline void init(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int grid, int x_,
-                              const PlanShared* sh) {
+  __device__ inline void init(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int x_, const PlanShared* sh,
+                              const SeqWin* wins) {
     x = x_;
     C = sh->C;
-    G = C < grid ? C : grid;
+    G = sh->G;
+    win = sh->kept ? wins : nullptr;
     if (x >= G || sh->b < 0) {
       pos = hi = 0;
       return;
@@ -324,17 +356,18 @@ struct ItemWalk {
       const int first = __shfl_sync(0xffffffffu, w_first, src), n = __shfl_sync(0xffffffffu, w_n, src);
       const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, src);
       const int i0 = tile * a.tpt, k = n - i0 < a.tpt ? n - i0 : a.tpt;
-      const int64_t kt = item_tiles(a, t0 + i0 + k, k), end = start + a.item_cost + kt;
+      const int kt = item_tiles(a, t0 + i0 + k, k);
+      const int64_t end = start + a.item_cost + kt;
       const int64_t y = hi < end ? hi : end;
       const int64_t k0 = pos - start - a.item_cost, k1 = y - start - a.item_cost;
       it->b = b;
       it->row0 = first + i0;
       it->ntok = k;
       it->t = t0 + i0 + 1;
-      it->R = group_of(t0 + i0 + k, a.s) - 1;
+      it->R = rows_below(a, t0 + i0 + k);
       it->kt0 = k0 > 0 ? (int)k0 : 0;
       it->kt1 = k1 > 0 ? (int)k1 : 0;
-      it->kt = (int)kt;
+      it->kt = kt;
       // outgoing parts (the item starts here and goes on) use slot 2 x + 1,
       // the others 2 x: a block has at most one of each
       it->slot = it->kt0 == 0 && it->kt1 == it->kt ? -1 : (it->kt0 == 0 ? 2 * x + 1 : 2 * x);
@@ -379,6 +412,7 @@ struct SplitDesc {
 // The first block that holds a key tile of an item at position `start`: the
 // last x with share_lo(x) <= start + item_cost.
 __device__ __forceinline__ int first_block(const PlanArgs& a, int64_t C, int64_t G, int64_t start) {
+  if (C < (1 << 20)) return (int)(((uint32_t)(start + a.item_cost + 1) * (uint32_t)G - 1u) / (uint32_t)C);
   return (int)(((start + a.item_cost + 1) * G - 1) / C);
 }
 
@@ -490,6 +524,6 @@ struct VerifyArgs {
   int32_t *n_keep, *next_token;
   int32_t* dev_err;
 };
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st);
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st);
 
 }  // namespace mtla

@@ -209,6 +209,8 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   a.plan.tpt = tpt < 16 ? tpt : 16;
   a.plan.q = (sh.tc ? PTC_COLS : PSN) / 8;
   a.plan.item_cost = 2;
+  a.plan.min_share = sh.tc ? 4 : 1;
+  a.plan.div_s = fast_div((uint32_t)dims->s);
   if (sh.tc) {
     PagedAttnMaps maps;
     if (!paged_maps(&maps, a)) return MTLA_ERR_CUDA;
@@ -246,7 +248,9 @@ mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, 
   a.n_keep = n_keep;
   a.next_token = next_token;
   a.dev_err = dev_err;
-  return from_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));
+  const int sms = current_device_sms();
+  if (sms <= 0) return MTLA_ERR_CUDA;
+  return from_cuda(launch_verify(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

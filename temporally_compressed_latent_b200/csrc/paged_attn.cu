@@ -23,7 +23,7 @@ namespace psimt {
 
 constexpr int NT = 256;
 
-size_t smem_bytes(int D) { return (size_t)(PSM + PSN) * (D + 4) * 4 + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + 256 * 8 + sizeof(PlanShared) + sizeof(Item) + 64; }
+size_t smem_bytes(int D) { return (size_t)(PSM + PSN) * (D + 4) * 4 + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + sizeof(PlanShared) + NT * sizeof(SeqWin) + sizeof(Item) + 64; }
 
 template <typename T> __device__ __forceinline__ void ld4(const T* p, float* v);
 template <> __device__ __forceinline__ void ld4<float>(const float* p, float* v) {
@@ -49,17 +49,18 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
   float* sm_l = sm_m + PSM;               // [PSM] running sums
   float* sm_a = sm_l + PSM;               // [PSM] rescale factors of the current tile
   PlanShared* plan = reinterpret_cast<PlanShared*>((reinterpret_cast<uintptr_t>(sm_a + PSM) + 15) & ~uintptr_t(15));
-  Item* sit = reinterpret_cast<Item*>(plan + 1);
+  SeqWin* wins = reinterpret_cast<SeqWin*>(plan + 1);
+  Item* sit = reinterpret_cast<Item*>(wins + NT);
   int* more = reinterpret_cast<int*>(sit + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = gridDim.x, x = blockIdx.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_block<NT>(a.c, a.p, a.plan, grid, x, a.dev_err, plan);
+  plan_block<NT>(a.c, a.p, a.plan, grid, x, a.dev_err, plan, wins);
   ItemWalk walk;
   walk.hi = walk.pos = 0;
-  if (warp == 0) walk.init(a.c, a.p, a.plan, grid, x, plan);
+  if (warp == 0) walk.init(a.c, a.p, a.plan, x, plan, wins);
   SplitDesc desc = {0, 0, 0, 0, 0, 0};  // (warp 0)
 
   for (;;) {
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       }
       auto put = [&](int i, int c, float v) {
         const int tok = i / a.H;
-        const int64_t g = v0 + c, seen = group_of(it.t + tok, a.plan.s) - 1;
+        const int64_t g = v0 + c, seen = rows_below(a.plan, it.t + tok);
         const bool vis = g < seen || g == R8 + tok;
         Ss[c * (PSM + 4) + i] = vis && tok < it.ntok ? v * a.scale_log2 : -INFINITY;
       };
@@ -247,93 +248,101 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
 // ----------------------------------------------------------------------------
 // Combine: block (g, y) finishes rows of the split item that ends in block g of
 // the attention grid: out = sum_x 2^(m_x - M) O_x / sum_x 2^(m_x - M) l_x over
-// its parts.  A thread takes four channels of a row; 256 threads take 4 rows at
-// once when parts are few, and one row with the parts split four ways when
-// they are many (a long cache under one token: latency of the loads bounds
-// it, eight in flight a thread).
+// its parts.  Four channels a thread, 64 threads a row, two rows at once when
+// parts are few, and one row with the parts split in two when they are many (a
+// long cache under one token: the loads' latency bounds it, four parts in
+// flight).  At 64 registers a thread a block fits beside the attention's and
+// waits there for its end.
 // ----------------------------------------------------------------------------
-constexpr int CNT = 256;
+constexpr int CNT = 128;
 
 template <typename T>
-__global__ void __launch_bounds__(CNT) paged_combine_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int g = blockIdx.x;
-  const SplitDesc d = a.part.desc[g];
-  const int live = d.ntok * a.H;
+  const SplitDesc* const d = a.part.desc + blockIdx.x;
+  const int live = d->ntok * a.H;
   if (live == 0) return;
-  __shared__ float red[4][64][5];
-  __shared__ float red_l[4];
-  const int parts = g - d.first + 1;  // every block between has one (their shares are not empty)
-  const int pg = parts > 16 ? 4 : 1;  // groups of parts
+  __shared__ float red[64][6];
+  const int first = d->first, parts = (int)blockIdx.x - first + 1;  // every block between has one (their shares are not empty)
+  const int64_t row0 = (int64_t)d->row0 * a.H;
+  const bool many = parts > 8;
   const int sub = threadIdx.x >> 6, q0 = threadIdx.x & 63;
-  const int grp = pg == 4 ? sub : 0;
-  const int rows_at_once = 4 / pg;
+  const int k_beg = many ? sub : 0, k_step = many ? 2 : 1, rows_at_once = many ? 1 : 2;
   for (int r0 = blockIdx.y * rows_at_once; r0 < live; r0 += gridDim.y * rows_at_once) {
-    const int row = r0 + (pg == 4 ? 0 : sub);
-    const bool on = row < live;
-    const int64_t orow = (int64_t)d.row0 * a.H + row;
+    const int row = r0 + (many ? 0 : sub);
     for (int e = 4 * q0; e < (a.r + 255) / 256 * 256; e += 256) {
-      float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-      if (on && e < a.r) {
-        for (int k0 = grp; k0 < parts; k0 += 8 * pg) {
-          float2 ml[8];
-          float4 o[8];
+      const bool on = row < live && e < a.r;
+      float M = -INFINITY, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on) {
+        for (int k0 = k_beg; k0 < parts; k0 += 4 * k_step) {
+          float2 ml[4];
+          float4 o[4];
+          float Mn = M;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int k = k0 + u * pg;
+          for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * k_step;
             ml[u] = make_float2(-INFINITY, 0.f);
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (k < parts) {
-              const int64_t prow = (int64_t)(2 * (d.first + k) + (k == 0 ? 1 : 0)) * a.rows + row;
+              const int64_t prow = (int64_t)(2 * (first + k) + (k == 0 ? 1 : 0)) * a.rows + row;
               ml[u] = a.part.ml[prow];
               o[u] = *reinterpret_cast<const float4*>(a.part.o + prow * a.r + e);
             }
           }
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float Mn = fmaxf(M, ml[u].x), ref = Mn == -INFINITY ? 0.f : Mn;
-            const float f0 = exp2f(M - ref), f1 = exp2f(ml[u].x - ref);
-            L = L * f0 + ml[u].y * f1;
-            // a part with nothing visible to this row holds no values of it
-            acc[0] = acc[0] * f0 + (f1 > 0.f ? o[u].x * f1 : 0.f);
-            acc[1] = acc[1] * f0 + (f1 > 0.f ? o[u].y * f1 : 0.f);
-            acc[2] = acc[2] * f0 + (f1 > 0.f ? o[u].z * f1 : 0.f);
-            acc[3] = acc[3] * f0 + (f1 > 0.f ? o[u].w * f1 : 0.f);
-            M = Mn;
+          for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, ml[u].x);
+          const float ref = Mn == -INFINITY ? 0.f : Mn, f = exp2f(M - ref);
+          M = Mn;
+          L *= f;
+          acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            // (a part with nothing visible to this row holds no values of it)
+            const float g = exp2f(ml[u].x - ref);
+            if (g > 0.f) {
+              L = fmaf(ml[u].y, g, L);
+              acc.x = fmaf(o[u].x, g, acc.x);
+              acc.y = fmaf(o[u].y, g, acc.y);
+              acc.z = fmaf(o[u].z, g, acc.z);
+              acc.w = fmaf(o[u].w, g, acc.w);
+            }
           }
         }
       }
-      if (pg == 4) {  // join the four groups (block-uniform branch)
+      if (many) {  // join the two halves of the parts (block-uniform branch)
         __syncthreads();
-        red[sub][q0][0] = acc[0];
-        red[sub][q0][1] = acc[1];
-        red[sub][q0][2] = acc[2];
-        red[sub][q0][3] = acc[3];
-        red[sub][q0][4] = M;
-        if (q0 == 0) red_l[sub] = L;
+        if (sub == 1) {
+          red[q0][0] = acc.x;
+          red[q0][1] = acc.y;
+          red[q0][2] = acc.z;
+          red[q0][3] = acc.w;
+          red[q0][4] = M;
+          red[q0][5] = L;
+        }
         __syncthreads();
-        if (sub == 0 && on && e < a.r) {
-          float Mt = -INFINITY;
-          for (int s = 0; s < 4; ++s) Mt = fmaxf(Mt, red[s][q0][4]);
-          L = 0.f;
-          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-          for (int s = 0; s < 4; ++s) {
-            const float f = exp2f(red[s][q0][4] - Mt);
-            L += red_l[s] * f;
-            for (int c = 0; c < 4; ++c) acc[c] += red[s][q0][c] * f;
-          }
+        if (sub == 0) {
+          const float M1 = red[q0][4], Mt = fmaxf(M, M1), ref = Mt == -INFINITY ? 0.f : Mt;
+          const float f0 = exp2f(M - ref), f1 = exp2f(M1 - ref);
+          L = L * f0 + red[q0][5] * f1;
+          acc.x = acc.x * f0 + red[q0][0] * f1;
+          acc.y = acc.y * f0 + red[q0][1] * f1;
+          acc.z = acc.z * f0 + red[q0][2] * f1;
+          acc.w = acc.w * f0 + red[q0][3] * f1;
           M = Mt;
         }
       }
-      if (on && e < a.r && (pg == 1 || sub == 0)) {
+      if (on && (!many || sub == 0)) {
         const float inv = 1.f / L;
+        const int64_t orow = row0 + row;
         if (a.lse && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
-        if (a.out_f32) {
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.r + e) =
-              make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+        const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (a.out_f32 || sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.r + e) = v;
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) st_elem(reinterpret_cast<T*>(a.out) + orow * a.r + e + c, acc[c] * inv);
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * a.r + e) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         }
       }
     }
@@ -394,8 +403,11 @@ cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cu
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int64_t rows = (int64_t)a.c.N * a.H < a.rows ? (int64_t)a.c.N * a.H : a.rows;
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(rows < 8 ? rows : 8));
+  // two rows at once a block, about four times (the rows of an item: the tokens
+  // of an average sequence, all heads)
+  const int64_t item = (a.c.N + (int64_t)a.c.B - 1) / a.c.B * a.H, rows = item < a.rows ? item : a.rows;
+  const int64_t y = rows <= 32 ? (rows + 1) / 2 : 16;
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)y);
   cfg.blockDim = dim3(psimt::CNT);
   cfg.stream = st;
   cfg.attrs = attr;

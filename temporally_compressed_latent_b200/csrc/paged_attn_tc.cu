@@ -19,6 +19,11 @@
 //    through a ring in shared memory, so no warp reads the sequence arrays on
 //    its own path.  Parts of items that a share boundary splits go to the
 //    workspace in fp32 and a second kernel joins them.
+//  * Three key tiles in flight, or four where no item has more than 64 live
+//    rows: the fourth then lies in the upper half of the queries' space.  A
+//    stage is free again only after its value MMA, about 2.3 us after it landed
+//    (score MMA, softmax, value MMA), so three stages gave 1.07 us a tile to a
+//    decode step.
 //  * Tiles are lists of 8-row groups: a group is nine [8 x 64 B] planes with the
 //    64-byte swizzle (4608 bytes, one TMA box), so a page of any multiple of 8
 //    rows feeds a key tile, the operand's 8-row stride is 4608 everywhere, and
@@ -47,7 +52,7 @@ constexpr int BN = 64;                 // columns of a key tile
 constexpr int GRP = D / 32 * 512;      // bytes of an 8-row group: nine planes of 8 x 64 B (4608)
 constexpr int QBYTES = BM / 8 * GRP;   // 73728
 constexpr int KBYTES = BN / 8 * GRP;   // 36864
-constexpr int KS = 3;                  // key-tile stages
+constexpr int KS = 3;                  // key-tile stages, and one more where queries take half their space
 constexpr int SMW = 8, EPW = 4;        // softmax and epilogue warps
 constexpr int TMA_WARP = SMW, SMMA_WARP = SMW + 1, PMMA_WARP = SMW + 2, SCHED_WARP = SMW + 3, EPI_WARP0 = SMW + 4;
 constexpr int NT = 32 * (SMW + 4 + EPW);
@@ -71,11 +76,14 @@ constexpr size_t OFF_K = OFF_Q + QBYTES;
 constexpr size_t OFF_OST = OFF_K + (size_t)KS * KBYTES;
 constexpr size_t OFF_XCH = OFF_OST + (size_t)EPW * OST_BYTES;  // maxima [2][2][BM], sums [2][2][BM], final maxima [2][BM]
 constexpr size_t OFF_RING = OFF_XCH + 10 * BM * 4;
-constexpr size_t OFF_PLAN = OFF_RING + RING * sizeof(RingItem);
+constexpr size_t OFF_WIN = OFF_RING + RING * sizeof(RingItem);
+constexpr size_t OFF_PLAN = OFF_WIN + PLAN_WINS * sizeof(SeqWin);
 constexpr size_t OFF_BAR = (OFF_PLAN + sizeof(PlanShared) + 15) / 16 * 16;
-constexpr int NBAR = 2 + 4 + 2 * KS + 3 * NSB + 3 + 2 * RING;
+constexpr int NBAR = 2 + 4 + 2 * (KS + 1) + 3 * NSB + 3 + 2 * RING;
 constexpr size_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr size_t SMEM = OFF_TMEM + 16 + 1024;
+static_assert(PLAN_WINS >= NT && OFF_WIN % 16 == 0, "a window a thread");
+static_assert(QBYTES == 2 * KBYTES && OFF_Q == 0, "a stage in the queries' upper half");
 static_assert(OFF_K % 1024 == 0 && GRP % 512 == 0 && KBYTES % 1024 == 0, "swizzle atoms");
 static_assert(SMEM <= 232448, "one block's shared memory (227 KB)");
 
@@ -118,9 +126,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   uint64_t* const q_empty = bar + 1;            // the item's last score MMA has read Q
   uint64_t* const stat_full = bar + 2;          // [2] an item's row maxima and sums are written
   uint64_t* const stat_empty = bar + 4;         // [2] the epilogue has read them
-  uint64_t* const k_full = bar + 6;             // [KS]
-  uint64_t* const k_empty = k_full + KS;        // [KS]
-  uint64_t* const s_full = k_empty + KS;        // [NSB]
+  uint64_t* const k_full = bar + 6;             // [KS + 1]
+  uint64_t* const k_empty = k_full + KS + 1;    // [KS + 1]
+  uint64_t* const s_full = k_empty + KS + 1;    // [NSB]
   uint64_t* const p_full = s_full + NSB;        // [NSB]
   uint64_t* const p_empty = p_full + NSB;       // [NSB] the value MMA has read P
   uint64_t* const o_full = p_empty + NSB;
@@ -143,7 +151,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       mbar_init(&stat_full[i], SMW);
       mbar_init(&stat_empty[i], EPW);
     }
-    for (int i = 0; i < KS; ++i) {
+    for (int i = 0; i < KS + 1; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
@@ -171,18 +179,18 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     prefetch_tmap(&mp.own);
     prefetch_tmap(&mp.cache);
   }
-  // operand rows and columns that nothing is loaded into multiply zeros or
-  // are never read, but must not hold NaN patterns of an earlier kernel
-  for (int i = tid; i < (int)(OFF_OST / 16); i += NT) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
-  plan_block<NT>(a.c, a.p, a.plan, gridDim.x, blockIdx.x, a.dev_err, plan);  // (holds block barriers)
+  SeqWin* const wins = reinterpret_cast<SeqWin*>(sm + OFF_WIN);
+  plan_block<NT>(a.c, a.p, a.plan, gridDim.x, blockIdx.x, a.dev_err, plan, wins);  // (holds block barriers)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t sQ = smem_u32(sm + OFF_Q), sK = smem_u32(sm + OFF_K);
+  const uint32_t sQ = smem_u32(sm + OFF_Q);
   const int H = a.H;
+  // key-tile stages: number, and the place of each
+  const uint32_t ns = plan->most * H <= BM / 2 ? KS + 1 : KS;
+  auto stage_off = [](uint32_t st) -> uint32_t { return st < (uint32_t)KS ? (uint32_t)OFF_K + st * KBYTES : (uint32_t)OFF_Q + QBYTES / 2; };
   bool ok = true;
 
   // the next item of the block's share, for one consumer warp
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   if (warp == SCHED_WARP) {
     // ======================= scheduler =======================
     ItemWalk walk;
-    walk.init(a.c, a.p, a.plan, gridDim.x, blockIdx.x, plan);
+    walk.init(a.c, a.p, a.plan, blockIdx.x, plan, wins);
     SplitDesc desc = {0, 0, 0, 0, 0, 0};
     uint32_t n = 0;
     for (;; ++n) {
@@ -240,23 +248,16 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     // Lane l of a batch of four key tiles looks up and loads group l: 32 table
     // entries are read at once, one batch ahead.
     const int32_t pool = (int32_t)(a.p.num_pages * a.p.page_rows);
-    uint32_t n = 0, kc = 0;
+    uint32_t n = 0, kc = 0, st = 0, ph = 0;      // stage of tile kc and its use's parity
     RingItem it;
     for (; take(n, it); ++n) {
       const int R8g = (it.R + 7) >> 3;
-      // pool row of this lane's group (past the pool: the box is filled with zeros)
-      auto group_row = [&](int g) -> int32_t {
-        if (g >= R8g) return 0;
-        const int k = (int)div32((uint32_t)(g * 8), a.p.div_rows);
-        const int32_t page = __ldg(a.p.table + (int64_t)it.b * a.p.table_pages + k);
-        if (page < 0 || page >= a.p.num_pages) {
-          set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
-          return pool;
-        }
-        return page * a.p.page_rows + (g * 8 - k * a.p.page_rows);
+      // the page of a group, read ahead of its use (-1: an own group)
+      auto look = [&](int g) -> int32_t {
+        if (g >= R8g) return -1;
+        return __ldg(a.p.table + (int64_t)it.b * a.p.table_pages + div32((uint32_t)(g * 8), a.p.div_rows));
       };
-      const int g0 = it.kt0 * (BN / 8);
-      int32_t cur = 0, nxt = group_row(g0 + lane);
+      int32_t cur = 0, nxt = look(it.kt0 * (BN / 8) + lane);
       // queries: the 8-row groups with live rows
       const int live = it.ntok * H, qg = (live + 7) >> 3;
       if (n > 0 && !warp_wait(q_empty, (n - 1) & 1)) { ok = false; break; }
@@ -270,18 +271,29 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         const int sub = (kt - it.kt0) & 3;
         if (sub == 0) {
           cur = nxt;
-          nxt = kt + 4 < it.kt1 ? group_row((kt + 4) * (BN / 8) + lane) : 0;
+          nxt = kt + 4 < it.kt1 ? look((kt + 4) * (BN / 8) + lane) : 0;
         }
-        const int st = kc % KS;
-        if (kc >= (uint32_t)KS && !warp_wait(&k_empty[st], ((kc / KS) & 1) ^ 1)) { ok = false; break; }
+        if (kc >= ns && !warp_wait(&k_empty[st], ph ^ 1)) { ok = false; break; }
         const int ng = tile_groups(R8g, it.ntok, kt);
         if (lane == 0) mbar_arrive_expect_tx(&k_full[st], ng * GRP);
         __syncwarp();
         const int gi = lane - 8 * sub, g = kt * (BN / 8) + gi;  // this lane's group of the tile
         if (gi >= 0 && gi < ng) {
-          uint8_t* dst = sm + OFF_K + st * KBYTES + gi * GRP;
-          if (g < R8g) tma_load_3d(dst, &mp.cache, 0, cur, 0, &k_full[st]);
+          uint8_t* dst = sm + stage_off(st) + gi * GRP;
+          if (g < R8g) {
+            // pool row of the group; of a page outside the pool: past its end, where the box fills with zeros
+            int32_t row = pool;
+            if (cur >= 0 && cur < a.p.num_pages)
+              row = cur * a.p.page_rows + (g * 8 - (int)div32((uint32_t)(g * 8), a.p.div_rows) * a.p.page_rows);
+            else
+              set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+            tma_load_3d(dst, &mp.cache, 0, row, 0, &k_full[st]);
+          }
           else tma_load_3d(dst, &mp.own, 0, it.row0 + 8 * (g - R8g), 0, &k_full[st]);
+        }
+        if (++st == ns) {
+          st = 0;
+          ph ^= 1;
         }
       }
       if (!ok) break;
@@ -289,25 +301,27 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
     // drain: no copy may still be writing shared memory when the block exits
     if (n > 0) warp_wait(q_full, (n - 1) & 1);
-    for (uint32_t j = kc > (uint32_t)KS ? kc - KS : 0; j < kc; ++j) warp_wait(&k_full[j % KS], (j / KS) & 1);
+    for (uint32_t j = kc > ns ? kc - ns : 0; j < kc; ++j) warp_wait(&k_full[j % ns], (j / ns) & 1);
   } else if (warp == SMMA_WARP || warp == PMMA_WARP) {
     // ======================= MMA issuers =======================
     const bool scores = warp == SMMA_WARP;
     const uint64_t dq0 = umma_desc(sQ, 16, GRP, 4);
-    const uint64_t dk0 = umma_desc(sK, 16, GRP, 4);
-    const uint64_t dv0 = umma_desc(sK, 512, GRP, 4);
-    uint32_t n = 0, kc = 0;
+    // (the stages' addresses are added to descriptors of the block's base: below 2^18, no carry)
+    const uint64_t dk0 = umma_desc(smem_u32(sm), 16, GRP, 4);
+    const uint64_t dv0 = umma_desc(smem_u32(sm), 512, GRP, 4);
+    uint32_t n = 0, kc = 0, st = 0, ph = 0;
     RingItem it;
     for (; take(n, it) && ok; ++n) {
       const int R8g = (it.R + 7) >> 3;
       if (scores && !warp_wait(q_full, n & 1)) { ok = false; break; }
       for (int kt = it.kt0; kt < it.kt1 && ok; ++kt, ++kc) {
-        const int st = kc % KS, sb = kc % NSB;
+        const int sb = kc % NSB;
+        const uint32_t off = stage_off(st);
         // columns in steps of 16 (two groups): a short last tile takes fewer
         const int n16 = (tile_groups(R8g, it.ntok, kt) + 1) >> 1;
         if (scores) {
           // S(j) = Q K(j)^T, once the value MMA of tile j - NSB has read the buffer
-          if (!warp_wait(&k_full[st], (kc / KS) & 1)) { ok = false; break; }
+          if (!warp_wait(&k_full[st], ph)) { ok = false; break; }
           if (kc >= (uint32_t)NSB && !warp_wait(&p_empty[sb], ((kc / NSB) & 1) ^ 1)) { ok = false; break; }
           tc_fence_after();
           const uint32_t idesc = umma_idesc_bf16(BM, 16, false, false) + ((uint32_t)(n16 - 1) * 2u << 17);
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint64_t ad = dq0 + (uint64_t)(((kk >> 1) * 512 + (kk & 1) * 32) >> 4);
-              const uint64_t bd = dk0 + (uint64_t)((st * KBYTES + (kk >> 1) * 512 + (kk & 1) * 32) >> 4);
+              const uint64_t bd = dk0 + (uint64_t)((off + (kk >> 1) * 512 + (kk & 1) * 32) >> 4);
               umma_bf16(tmem + s_col(sb), ad, bd, idesc, kk > 0 ? 1u : 0u);
             }
             umma_commit(&s_full[sb]);
@@ -328,7 +342,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           tc_fence_after();
           if (elect_one()) {
             for (int kk = 0; kk < n16; ++kk) {
-              const uint64_t bd = dv0 + (uint64_t)((st * KBYTES + kk * 2 * GRP) >> 4);
+              const uint64_t bd = dv0 + (uint64_t)((off + kk * 2 * GRP) >> 4);
               umma_bf16_ts(tmem + O_COL, tmem + s_col(sb) + 8 * kk, bd, IDESC_O, (kt > it.kt0 || kk > 0) ? 1u : 0u);
             }
             umma_commit(&k_empty[st]);
@@ -337,6 +351,10 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           }
         }
         __syncwarp();
+        if (++st == ns) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     }
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
@@ -347,9 +365,11 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   } else if (warp >= EPI_WARP0) {
     // ======================= epilogue warps =======================
     // warp EPI_WARP0 + e owns rows 32 e .. 32 e + 31 (TMEM lane quarter e): a
-    // whole item's rows leave as out = O / l, a part's as O with (m, l).  64
-    // bytes of 32 rows at a time go through a staging block in shared memory
-    // (64-byte swizzle), so that a store writes 64 contiguous bytes of 8 rows.
+    // whole item's rows leave as out = O / l, a part's as O with (m, l).  bf16
+    // rows go 64 bytes of 32 rows at a time through a staging block in shared
+    // memory (64-byte swizzle), so that a store writes 64 contiguous bytes of 8
+    // rows; fp32 rows (parts: few live rows in a decode step, where the chain of
+    // 16 such passes took 2 us) go straight from the registers.
     const int qe = warp - EPI_WARP0, i = qe * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(qe * 32) << 16);
     const uint32_t ost = smem_u32(sm + OFF_OST + (size_t)qe * OST_BYTES);
@@ -377,11 +397,43 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         if (lane == 0) mbar_arrive(o_empty);
         continue;
       }
-      const bool wide = part || a.out_f32;       // fp32 rows: 16 channels are 64 bytes; bf16 rows: 32
-      const int pitch = wide ? R * 4 : R * 2;
-      uint8_t* const base = (part ? reinterpret_cast<uint8_t*>(a.part.o) : static_cast<uint8_t*>(a.out)) +
-                            (row - lane) * (int64_t)pitch;  // the quarter's first row
-      auto put = [&](const uint32_t* w, int block) {
+      if (part || a.out_f32) {                   // fp32: a lane's row, 128 bytes of it at a time
+        float* const dst = (part ? a.part.o : static_cast<float*>(a.out)) + row * R;
+#pragma unroll 1
+        for (int c = 0; c < R / 64; ++c) {
+          uint32_t ov[64];
+          tmem_ld32(lane_base + O_COL + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&ov[0]));
+          tmem_ld32(lane_base + O_COL + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[32]));
+          tmem_wait_ld();
+          if (c == R / 64 - 1) {                 // the last read of O: the next item's value MMAs may start
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty);
+          }
+          if (i < live) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4)
+              *reinterpret_cast<float4*>(dst + c * 64 + e) =
+                  make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
+                              __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
+          }
+        }
+        continue;
+      }
+      __nv_bfloat16* const base = static_cast<__nv_bfloat16*>(a.out) + (row - lane) * R;  // the quarter's first row
+#pragma unroll 1
+      for (int c = 0; c < R / 32; ++c) {
+        uint32_t ov[32], w[16];
+        tmem_ld32(lane_base + O_COL + c * 32, ov);
+        tmem_wait_ld();
+        if (c == R / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
         __syncwarp();                            // the previous block's transposed reads are done
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -398,30 +450,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
             const uint32_t off = (uint32_t)r * 64u + ((((uint32_t)tq) ^ (((uint32_t)r >> 1) & 3u)) << 4);
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(ost + off));
-            *reinterpret_cast<uint4*>(base + (int64_t)r * pitch + block * 64 + tq * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(base + (int64_t)r * R + c * 32 + tq * 8) = make_uint4(v[0], v[1], v[2], v[3]);
           }
-        }
-      };
-#pragma unroll 1
-      for (int c = 0; c < R / 32; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(lane_base + O_COL + c * 32, ov);
-        tmem_wait_ld();
-        if (c == R / 32 - 1) {  // the last read of O: the next item's value MMAs may start
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
-        if (wide) {
-          put(ov, 2 * c);
-          put(ov + 16, 2 * c + 1);
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]), __uint_as_float(ov[2 * e + 1]));
-          put(w, c);
         }
       }
     }
@@ -437,7 +467,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     const int qw = warp & 3, hf = warp >> 2, i = qw * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(qw * 32) << 16);
     const float sl2 = a.scale_log2;
-    uint32_t n = 0, kc = 0;
+    uint32_t n = 0, kc = 0, st = 0;
     for (;; ++n) {
       RingItem it;
       const bool more = take(n, it);
@@ -445,11 +475,13 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       const int live = it.ntok * H, tok = i / H, R8 = (it.R + 7) & ~7;
       const bool on = i < live;
       // columns this row sees: below `seen`, and its own
-      const int seen = on ? (int)(group_of(it.t + tok, a.plan.s) - 1) : 0;
+      // (rows without a token see everything: what they hold is never stored,
+      // and they do not keep their warp on the masked path)
+      const int seen = on ? rows_below(a.plan, it.t + tok) : 0x7fffffff;
       const int own = on ? R8 + tok : -1;
       float m_run = -INFINITY, l = 0.f;  // l: this half's sum
       for (int kt = it.kt0; kt < it.kt1; ++kt, ++kc) {
-        const int sb = kc % NSB, xb = kc & 1, st = kc % KS;
+        const int sb = kc % NSB, xb = kc & 1;
         if (ok && !warp_wait(&s_full[sb], (kc / NSB) & 1)) ok = false;
         tc_fence_after();
         if (kt * BN + BN > it.R) {
@@ -458,7 +490,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           for (int r = warp; r < rows; r += SMW) {
             const int v = kt * BN + r;
             if (v >= it.R && (v < R8 || v >= R8 + it.ntok))
-              *reinterpret_cast<uint4*>(sm + OFF_K + st * KBYTES + (r >> 3) * GRP + (lane >> 2) * 512 + (r & 7) * 64 +
+              *reinterpret_cast<uint4*>(sm + stage_off(st) + (r >> 3) * GRP + (lane >> 2) * 512 + (r & 7) * 64 +
                                         (lane & 3) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -467,25 +499,27 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           uint32_t sr[32];
           tmem_ld32(lane_base + s_col(sb) + 32 * hf, sr);
           tmem_wait_ld();
-          const int c0 = kt * BN + 32 * hf, nvis = seen - c0, self = own - c0;
           float x[32];
-          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (kt * BN + BN > it.R) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = c < nvis || c == self ? __uint_as_float(sr[c]) * sl2 : -INFINITY;
-          } else {
+          for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sr[c]);
+          const int c0 = kt * BN + 32 * hf, nvis = seen - c0;
+          if (!__all_sync(0xffffffffu, nvis >= 32)) {  // some row does not see all of these columns
+            const int self = own - c0;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = c < nvis ? __uint_as_float(sr[c]) * sl2 : -INFINITY;
+            for (int c = 0; c < 32; ++c)
+              if (!(c < nvis || c == self)) x[c] = -INFINITY;
           }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four independent chains
 #pragma unroll
           for (int c = 0; c < 32; ++c) mq[c & 3] = fmaxf(mq[c & 3], x[c]);
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          // (the scale is positive: the maximum of the scaled scores)
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
           xmax[(xb * 2 + hf) * BM + i] = mx;
           tc_fence_before();
           named_bar(1 + qw, 64);
           tc_fence_after();
           const float rmx = fmaxf(mx, xmax[(xb * 2 + (hf ^ 1)) * BM + i]);
-          const bool grow = rmx > m_run + 8.f;
+          const bool grow = on && rmx > m_run + 8.f;
           const bool resc = grow && m_run != -INFINITY;
           if (kt > it.kt0 && __any_sync(0xffffffffu, resc)) {
             const uint32_t jp = kc - 1;
@@ -511,7 +545,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           float lq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
-            const float p0 = ex2_approx(x[c] - mref), p1 = ex2_approx(x[c + 1] - mref);
+            const float p0 = ex2_approx(fmaf(x[c], sl2, -mref)), p1 = ex2_approx(fmaf(x[c + 1], sl2, -mref));
             lq[(c >> 1) & 3] += p0 + p1;
             pk[c >> 1] = pack_bf16x2(p0, p1);
           }
@@ -522,6 +556,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[sb]);
+        if (++st == ns) st = 0;
       }
       const int sb2 = n & 1;
       if (ok && n >= 2 && !warp_wait(&stat_empty[sb2], ((n >> 1) & 1) ^ 1)) ok = false;

@@ -7,16 +7,18 @@
 // all are kept, from p of the chunk's last row.  It is drawn by inversion: the
 // lowest index whose running sum exceeds u times the sum.
 //
-// A cluster of CL blocks takes a sequence: only one row of p and of q is read
-// (the drafts' probabilities are gathers), so the vocabulary is split over the
-// cluster for its latency and bandwidth, and the blocks exchange their sums
+// A cluster of up to 8 blocks takes a sequence: only one row of p and of q is
+// read (the drafts' probabilities are gathers), so the vocabulary is split over
+// the cluster for its latency and bandwidth, and the blocks exchange their sums
 // through distributed shared memory.  A warp sums 256 entries at a time, eight
 // a lane, and notes each sum; after the exchange the one block that holds the
-// drawn index scans its sums and reads one such run again.  Sums are in double
-// precision: the running sum over 10^5 entries of size 10^-5 must place the
-// border between neighbours, which 24 bits would miss once in a hundred draws.
-// They are trees of depth three in a lane and five across it (an addition in
-// double takes tens of cycles: a chain of 32 cost 2 us a step here).
+// drawn index scans its sums and reads one such run again.  Runs are cut at
+// 16-byte boundaries of p's row, so rows of any alignment are read four entries
+// a load.  Sums are in double precision: the running sum over 10^5 entries of
+// size 10^-5 must place the border between neighbours, which 24 bits would miss
+// once in a hundred draws.  They are trees of depth three in a lane and five
+// across it (an addition in double takes tens of cycles: chains of 32 made one
+// sequence's call 17 us instead of 5).
 // Bound by the two rows' HBM reads (large batches) or by the chain of four
 // dependent reads and the cluster's barriers (small ones).
 #include <cooperative_groups.h>
@@ -27,11 +29,10 @@ namespace mtla {
 namespace vfy {
 
 namespace cg = cooperative_groups;
-constexpr int CL = 8;
-constexpr int NT = 512, NW = NT / 32;
+constexpr int MAXCL = 8;
+constexpr int NT = 256, NW = NT / 32, BLOCKS = 4;   // threads; resident blocks an SM
 constexpr int RUN = 256;                            // entries a warp sums at a time
-constexpr int MAXV = 1 << 22;
-constexpr int MAXRUNS = MAXV / RUN / CL;            // runs of a block: 2048
+constexpr int MAXRUNS = 2304;                       // runs of a block (2^22 entries over 8 blocks: 2049)
 
 // entries that are NaN, infinite or not above zero count as zero
 __device__ __forceinline__ float clean(float x) { return x > 0.f && x <= 3.4028234663852886e38f ? x : 0.f; }
@@ -50,55 +51,58 @@ __device__ __forceinline__ double warp_scan(double x) {  // inclusive
   return x;
 }
 
-// What the next token is drawn from.
+// What the next token is drawn from.  Entries are counted from the 16-byte
+// boundary at or before the row's start: position j is entry j - shift.
 struct Weights {
   const float *p, *q;   // q: null where p alone counts
-  int V, hole;          // hole: an index without weight, or -1
-  // eight entries of a run starting at v0: lane l's are v0 + 4 l .. + 3 and v0 +
-  // 128 + 4 l .. + 3 (in index order a lane holds two quadruples)
-  template <bool VEC>
-  __device__ __forceinline__ void load(int v0, float (&a)[8], float (&b)[8]) const {
+  int V, hole;          // hole: an entry without weight, or -1
+  int shift;            // entries between that boundary and the row of p
+  bool qvec;            // q's row has the same shift
+  // eight positions of a run starting at j0: lane l's are j0 + 4 l .. + 3 and
+  // j0 + 128 + 4 l .. + 3
+  __device__ __forceinline__ void load(int j0, float (&a)[8], float (&b)[8]) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int v = v0 + 128 * h + 4 * lane;
-      if (VEC && v + 4 <= V) {
+      const int v = j0 + 128 * h + 4 * lane - shift;
+      const bool whole = v >= 0 && v + 4 <= V;
+      if (whole) {
         const float4 x = __ldg(reinterpret_cast<const float4*>(p + v));
         a[4 * h] = x.x; a[4 * h + 1] = x.y; a[4 * h + 2] = x.z; a[4 * h + 3] = x.w;
-        if (q) {
-          const float4 y = __ldg(reinterpret_cast<const float4*>(q + v));
-          b[4 * h] = y.x; b[4 * h + 1] = y.y; b[4 * h + 2] = y.z; b[4 * h + 3] = y.w;
-        }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[4 * h + e] = v + e < V ? __ldg(p + v + e) : 0.f;
-          if (q) b[4 * h + e] = v + e < V ? __ldg(q + v + e) : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) a[4 * h + e] = v + e >= 0 && v + e < V ? __ldg(p + v + e) : 0.f;
+      }
+      if (!q) continue;
+      if (whole && qvec) {
+        const float4 y = __ldg(reinterpret_cast<const float4*>(q + v));
+        b[4 * h] = y.x; b[4 * h + 1] = y.y; b[4 * h + 2] = y.z; b[4 * h + 3] = y.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[4 * h + e] = v + e >= 0 && v + e < V ? __ldg(q + v + e) : 0.f;
       }
     }
   }
-  __device__ __forceinline__ void weigh(int v0, const float (&a)[8], const float (&b)[8], double (&w)[8]) const {
+  __device__ __forceinline__ void weigh(int j0, const float (&a)[8], const float (&b)[8], double (&w)[8]) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float x = clean(a[k]), y = q ? clean(b[k]) : 0.f;
       // (a float difference has the sign of the exact one)
       w[k] = x > y ? (double)x - (double)y : 0.0;
-      if (v0 + 128 * (k >> 2) + 4 * lane + (k & 3) == hole) w[k] = 0.0;
+      if (j0 + 128 * (k >> 2) + 4 * lane + (k & 3) - shift == hole) w[k] = 0.0;
     }
   }
 };
 
-template <bool VEC>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ double run_sum[MAXRUNS];
   __shared__ double warp_total[NW];
-  __shared__ double totals[2][CL];                  // every block's sum, written by the blocks themselves
+  __shared__ double totals[2][MAXCL];                 // every block's sum, written by the blocks themselves
   __shared__ int first_drop;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster.block_rank(), b = blockIdx.x / CL;
+  const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / CL;
 
   const int s0 = a.tok_start[b], s1 = a.tok_start[b + 1];
   const int first = s0 < 0 ? 0 : (s0 < a.N ? s0 : a.N);
@@ -140,10 +144,12 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
   w.p = a.p + (int64_t)(first + drop) * a.ld_p;
   w.q = a.q && dropped ? a.q + (int64_t)(first + drop) * a.ld_q : nullptr;
   w.V = a.V;
+  w.shift = (int)(reinterpret_cast<uintptr_t>(w.p) >> 2 & 3);
+  w.qvec = w.q && (int)(reinterpret_cast<uintptr_t>(w.q) >> 2 & 3) == w.shift;
   // certain drafts (no q): the residual is p without the dropped token
   w.hole = !a.q && dropped ? a.tokens[first + drop + 1] : -1;
 
-  const int runs = (a.V + RUN - 1) / RUN, per = (runs + CL - 1) / CL;
+  const int runs = (a.V + w.shift + RUN - 1) / RUN, per = (runs + CL - 1) / CL;
   const int r_beg = rank * per < runs ? rank * per : runs, r_end = r_beg + per < runs ? r_beg + per : runs;
   const int mine = r_end - r_beg;
   double total = 0.0;
@@ -155,7 +161,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
       float pa[2][8], qa[2][8];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (r + h * NW < mine) w.load<VEC>((r_beg + r + h * NW) * RUN, pa[h], qa[h]);
+        if (r + h * NW < mine) w.load((r_beg + r + h * NW) * RUN, pa[h], qa[h]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (r + h * NW < mine) {
@@ -230,7 +236,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
   const int v0 = (r_beg + pick) * RUN;
   float pa[8], qa[8];
   double x[8];
-  w.load<VEC>(v0, pa, qa);
+  w.load(v0, pa, qa);
   w.weigh(v0, pa, qa, x);
   c = at;
   int token = -1;
@@ -242,10 +248,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
     int hit = -1, lastp = -1;
 #pragma unroll
     for (int k = 3; k >= 0; --k)
-      if (x[4 * h + k] > 0.0 && run[k] > target) hit = v0 + 128 * h + 4 * lane + k;
+      if (x[4 * h + k] > 0.0 && run[k] > target) hit = v0 + 128 * h + 4 * lane + k - w.shift;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (x[4 * h + k] > 0.0) lastp = v0 + 128 * h + 4 * lane + k;
+      if (x[4 * h + k] > 0.0) lastp = v0 + 128 * h + 4 * lane + k - w.shift;
     const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0), some = __ballot_sync(0xffffffffu, lastp >= 0);
     if (hits) {
       token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
@@ -260,14 +266,25 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NT) verify_kernel(c
 
 }  // namespace vfy
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  // rows that all start on 16 bytes are read four entries at a time
-  const bool vec = (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && a.ld_p % 4 == 0 &&
-                   (!a.q || ((reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.ld_q % 4 == 0));
-  const unsigned grid = (unsigned)a.B * vfy::CL;
-  if (vec) vfy::verify_kernel<true><<<grid, vfy::NT, 0, st>>>(a);
-  else vfy::verify_kernel<false><<<grid, vfy::NT, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
+  // As many blocks a sequence as leave all of them resident at once (a
+  // sequence's chain of latencies is then paid once): 96 sequences of 131072
+  // entries take XX us with 8 blocks each, YY with 6; at least as many as keep
+  // a block's notes in its shared memory.
+  int cl = sms * vfy::BLOCKS / a.B;
+  const int least = (a.V / vfy::RUN + 2) / vfy::MAXRUNS + 1;
+  cl = cl < least ? least : (cl > vfy::MAXCL ? vfy::MAXCL : cl);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cl;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B * (unsigned)cl);
+  cfg.blockDim = dim3(vfy::NT);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, vfy::verify_kernel, a);
 }
 
 }  // namespace mtla
