@@ -84,6 +84,28 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* tok_start, int B, in
   return lo;
 }
 
+// The sequences of token rows base + lane + 32 m, m < NM (b[m] = -1: none).
+// A search for the first row, then the following starts 32 at a time.
+template <int NM>
+__device__ __forceinline__ void warp_sequences(const ChunkDev& c, int64_t base, int (&b)[NM]) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = base > 0 ? base : 0, last = base + 32 * NM - 1;
+  int b0 = warp_find_seq(c.tok_start, c.B, (int)(first < c.N ? first : c.N));
+#pragma unroll
+  for (int m = 0; m < NM; ++m) b[m] = b0;
+  for (int bb = b0 + 1; bb < c.B; bb += 32) {
+    const int v = bb + lane < c.B ? c.tok_start[bb + lane] : 0x7fffffff;
+    if (__shfl_sync(0xffffffffu, v, 0) > last) break;
+    for (int k = 0; k < 32; ++k) {
+      const int sk = __shfl_sync(0xffffffffu, v, k);
+      if (sk > last) break;
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+        if (sk <= base + lane + 32 * m) b[m] = bb + k;
+    }
+  }
+}
+
 // ----------------------------------------------------------------------------
 // RoPE angles: channel pair k turns by pos * base^(-2k/d_R).  The host passes
 // the angle of one position as a fraction of a turn in 64-bit fixed point (its
@@ -174,6 +196,8 @@ __device__ __forceinline__ int item_tiles(const PlanArgs& a, int64_t t, int k) {
 }
 // weight of a sequence's first m items (chunk of n tokens after t0)
 __device__ inline int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int64_t m) {
+  if (m == 0) return 0;
+  if (n <= a.tpt) return a.item_cost + item_tiles(a, t0 + n, n);  // one item
   const int64_t full = n / a.tpt, k = m < full ? m : full;
   int64_t w = m * a.item_cost;
   if (k == 1) w += item_tiles(a, t0 + a.tpt, a.tpt);
@@ -198,6 +222,7 @@ struct Item {
 // Blocks that get a share: no more than give each min_share of the weight C.
 __device__ __forceinline__ int64_t share_blocks(const PlanArgs& a, int64_t C, int grid) {
   if (C >= (int64_t)a.min_share * grid) return grid;
+  if (C <= 2 * a.min_share) return C > 0;  // too little to pay for joining parts
   return ((int)C + a.min_share - 1) / a.min_share;
 }
 // Shares: block x of G takes [C x / G, C (x + 1) / G).
@@ -333,7 +358,7 @@ struct ItemWalk {
     const int n = __shfl_sync(0xffffffffu, w_n, 0);
     const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, 0), rem = pos - sh->before;
     const int lane = threadIdx.x & 31;
-    int lo = 0, up = (n + a.tpt - 1) / a.tpt;
+    int lo = 0, up = n <= a.tpt ? 1 : (n + a.tpt - 1) / a.tpt;
     while (up - lo > 1) {
       const int step = (up - lo - 1 + 31) / 32, at = lo + 1 + lane * step;
       const bool le = at < up && items_weight(a, t0, n, at) <= rem;
@@ -484,7 +509,8 @@ struct PagedAppendArgs {
   int H, r, d_R, s;
   FastDiv div_s;
   int rotate;  // 0: keys and queries are rotated already
-  int tt;      // tokens of a block's tile
+  int tt;      // tokens of a block's tile (generic kernel)
+  int halo;    // token rows before a tile that its block always computes too, or -1: as many as its first group needs
 };
 // The chunk window the append takes: a sequence that does not fit its table or
 // the P table (or has a negative time) takes none.  Times of a chunk are below
@@ -504,6 +530,34 @@ __device__ __forceinline__ AppendWin append_win(const PagedAppendArgs& a, int b,
   SeqWin w = seq_win(a.c, b);
   append_fit(a, w, report);
   return w;
+}
+// The sequence (-1: none) and append window of token row base + lane, by a whole
+// warp: one round of loads for up to 32 sequences (a lane each), else a search
+// and a second round.
+__device__ __forceinline__ void warp_windows(const PagedAppendArgs& a, int64_t base, int& b, AppendWin& w) {
+  const int lane = threadIdx.x & 31;
+  if (a.c.B <= 32) {
+    AppendWin mine;
+    mine.first = mine.n = 0;
+    mine.t0 = 0;
+    int start = 0x7fffffff;
+    if (lane < a.c.B) {
+      start = a.c.tok_start[lane];
+      mine = append_win(a, lane, false);
+    }
+    b = -1;
+    for (int k = 0; k < a.c.B; ++k)
+      if (__shfl_sync(0xffffffffu, start, k) <= base + lane) b = k;
+    const int from = b < 0 ? 0 : b;
+    w.first = __shfl_sync(0xffffffffu, mine.first, from);
+    w.n = __shfl_sync(0xffffffffu, mine.n, from);
+    w.t0 = __shfl_sync(0xffffffffu, mine.t0, from);
+  } else {
+    int v[1];
+    warp_sequences<1>(a.c, base, v);
+    b = v[0];
+    w = append_win(a, b < 0 ? 0 : b, false);
+  }
 }
 cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st);
 

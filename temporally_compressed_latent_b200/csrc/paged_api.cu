@@ -1,6 +1,7 @@
 // C ABI of the paged calls: argument checks, kernel selection, launches.  See
 // include/mtla.h for the contract of every entry point.
 #include <math.h>
+#include <string.h>
 
 #include "paged.cuh"
 
@@ -79,6 +80,27 @@ bool paged_maps(PagedAttnMaps* m, const PagedAttnArgs& a) {
          row_groups_map(&m->cache, a.p.pages, a.p.num_pages * a.p.page_rows, a.p.row_stride * 2, 9);
 }
 
+// The angles of one position; a thread keeps the last ones (16 long powers cost
+// as much as the launch).
+void rope_table(double base, int d_R, RopeTable* t) {
+  struct Last {
+    double base = 0.0;
+    int d_R = 0;
+    RopeTable t;
+  };
+  thread_local Last last;
+  if (last.base != base || last.d_R != d_R) {
+    for (int k = 0; k < d_R / 2; ++k) {
+      const long double turn = powl((long double)base, -2.0L * k / d_R) / 6.283185307179586476925286766559L;
+      const long double part = turn - floorl(turn);  // in [0, 1)
+      last.t.turns[k] = (uint64_t)(part * 18446744073709551616.0L);
+    }
+    last.base = base;
+    last.d_R = d_R;
+  }
+  memcpy(t->turns, last.t.turns, (size_t)(d_R / 2) * sizeof(uint64_t));
+}
+
 // The append's tensor-core kernel: the widths its tiles are laid out for, groups
 // that fit beside half a tile, and enough tokens that its start (W_c into TMEM)
 // costs less than the generic kernel's arithmetic.
@@ -133,12 +155,7 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   a.m.P = merge->P;
   a.m.J_max = merge->J_max;
   a.rotate = rope_base > 0.0 && dims->d_R > 0;
-  if (a.rotate)
-    for (int k = 0; k < dims->d_R / 2; ++k) {
-      const long double turn = powl((long double)rope_base, -2.0L * k / dims->d_R) / 6.283185307179586476925286766559L;
-      const long double part = turn - floorl(turn);  // in [0, 1)
-      a.rope.turns[k] = (uint64_t)(part * 18446744073709551616.0L);
-    }
+  if (a.rotate) rope_table(rope_base, dims->d_R, &a.rope);
   a.q_rope = dims->d_R > 0 ? q_rope : nullptr;
   a.q_rope_out = q_rope_out;
   a.tail_in = tail_in;

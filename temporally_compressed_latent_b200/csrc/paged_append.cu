@@ -11,10 +11,16 @@
 // to, and 32 of the row's D channels.  Its 256 threads split the r latents of
 // the gate contraction eight ways; a thread keeps its 1/8 of a channel's
 // column of W_c in registers for the whole tile, so W_c is read once a block.
-// A tile that begins inside a group starts that many tokens earlier (at most
-// s - 1) and recomputes their entries, so that no block waits for another; the
-// sums run from the group's start in token order in every tile, which makes
-// them independent of the tiling.  Few tokens: the chain of loads bounds it.
+// A tile that begins inside a group recomputes the entries of the group's
+// earlier tokens (at most s - 1), so that no block waits for another; the sums
+// run from the group's start in token order in every tile, which makes them
+// independent of the tiling.
+//
+// Few tokens: the chain of dependent reads bounds it.  So W_c, the latents of
+// the first round (with a short stride the rows before a tile are taken
+// whether needed or not, and no read waits to know) and the sequences' windows
+// are all requested at the start, and P, the tails, the RoPE keys and the table
+// entries as soon as the windows are known, before the products.
 #include "paged.cuh"
 
 namespace mtla {
@@ -23,22 +29,31 @@ namespace pap {
 constexpr int NT = 256, NW = NT / 32;
 constexpr int U = 16;                // tokens of one round
 
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 x = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
 // One token's place, as the block's threads share it.
 struct Tok {
-  int64_t j;        // group (1-based)
-  int64_t prow;     // pool row to write, or -1
-  int seq;          // -1: no sequence takes this row
-  uint8_t opens;    // the running sum starts at this token's entry
-  uint8_t carry;    // ... or at tail_in plus it
-  uint8_t last;     // last token of its sequence's chunk
-  uint8_t out;      // stored by this block (not a recomputed one)
+  uint32_t group, pos;  // 0-based group and time
+  int seq;              // -1: no sequence takes this row
+  uint8_t opens;        // the running sum starts at this token's entry
+  uint8_t carry;        // ... with tail_in added
+  uint8_t last;         // last token of its sequence's chunk
+  uint8_t row;          // it writes a cache row
 };
 
-struct Smem {
+struct alignas(16) Smem {
   float part[NW][U][32];
   float v[U][32];       // gated entries, then sums
   Tok tok[U];
+  int64_t i0;
 };
+static_assert(sizeof(Smem) % 16 == 0 && sizeof(Tok) == 16, "the latents behind it are read four at a time");
 
 // KPT: latents per warp, at least r / 8
 template <typename T, int KPT>
@@ -67,20 +82,24 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
     // ---- RoPE queries: one warp a token, its d_R / 2 angles once for all heads
     const int i = (blockIdx.x - gate_blocks) * NW + warp;
     if (i >= a.c.N) return;
-    const int b = warp_find_seq(a.c.tok_start, a.c.B, i);
-    if (b < 0) return;
-    const AppendWin w = append_win(a, b, false);
-    if (i - w.first >= w.n) return;
+    int b;
+    AppendWin w;
+    warp_windows(a, i, b, w);
+    b = __shfl_sync(0xffffffffu, b, 0);
+    w.first = __shfl_sync(0xffffffffu, w.first, 0);
+    w.n = __shfl_sync(0xffffffffu, w.n, 0);
+    w.t0 = __shfl_sync(0xffffffffu, w.t0, 0);
+    if (b < 0 || i - w.first >= w.n) return;
     const uint32_t pos = (uint32_t)(w.t0 + (i - w.first));
     const T* src = reinterpret_cast<const T*>(a.q_rope) + (int64_t)i * a.H * a.d_R;
     T* dst = reinterpret_cast<T*>(a.q_rope_out) + (int64_t)i * a.H * a.d_R;
-    for (int k = lane; k < a.d_R / 2; k += 32) {
-      const float2 cs = a.rotate ? rope_cos_sin(pos, a.rope.turns[k]) : make_float2(1.f, 0.f);
-      for (int h = 0; h < a.H; ++h) {
-        const float x0 = ld_f32(src + h * a.d_R + 2 * k), x1 = ld_f32(src + h * a.d_R + 2 * k + 1);
-        st_elem(dst + h * a.d_R + 2 * k, x0 * cs.x - x1 * cs.y);
-        st_elem(dst + h * a.d_R + 2 * k + 1, x0 * cs.y + x1 * cs.x);
-      }
+    const int pairs = a.d_R / 2;
+    // a lane's pairs: k, k + 32, ... of all heads in a row
+    for (int e = lane; e < a.H * pairs; e += 32) {
+      const float x0 = ld_f32(src + 2 * e), x1 = ld_f32(src + 2 * e + 1);
+      const float2 cs = a.rotate ? rope_cos_sin(pos, a.rope.turns[e % pairs]) : make_float2(1.f, 0.f);
+      st_elem(dst + 2 * e, x0 * cs.x - x1 * cs.y);
+      st_elem(dst + 2 * e + 1, x0 * cs.y + x1 * cs.x);
     }
     return;
   }
@@ -100,104 +119,126 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
   }
   const float bc = live ? __ldg(a.m.b_c + ch) : 0.f;
 
-  // the tile's first group: recompute its earlier tokens of this chunk
-  int64_t i0 = i_beg;
-  {
-    const int b = warp_find_seq(a.c.tok_start, a.c.B, (int)i_beg);
-    if (b >= 0) {
-      const AppendWin w = append_win(a, b, false);
-      const int64_t place = i_beg - w.first;
-      if (place < w.n) {
-        const int64_t in_group = (w.t0 + place) % s;
-        i0 = i_beg - (in_group < place ? in_group : place);
+  // the first token row: before the tile, where its first group may begin
+  int64_t i0 = i_beg - a.halo;
+  if (a.halo < 0) {
+    if (warp == 0) {
+      int b;
+      AppendWin w;
+      warp_windows(a, i_beg, b, w);
+      if (lane == 0) {
+        const int64_t place = i_beg - w.first;
+        int64_t back = 0;
+        if (b >= 0 && place < w.n) {
+          const uint32_t t = (uint32_t)(w.t0 + place), in = t - div32(t, a.div_s) * (uint32_t)s;
+          back = in < place ? (int64_t)in : place;
+        }
+        sm.i0 = i_beg - back;
       }
     }
+    __syncthreads();
+    i0 = sm.i0;
   }
   float run = 0.f;  // (warp 0) the running sum of this thread's channel
   for (int64_t r0 = i0; r0 < i_end; r0 += U) {
-    // places of the round's tokens: two a warp
-    for (int u = warp; u < U; u += NW) {
-      const int64_t i = r0 + u;
-      Tok t;
-      t.seq = -1;
-      t.j = 1;
-      t.prow = -1;
-      t.opens = t.carry = t.last = t.out = 0;
-      if (i < i_end) {
-        const int b = warp_find_seq(a.c.tok_start, a.c.B, (int)i);
-        if (b >= 0) {
-          const AppendWin w = append_win(a, b, false);
-          const int place = (int)(i - w.first);
-          if (place < w.n) {
-            const uint32_t tm = (uint32_t)(w.t0 + place);  // 0-based time
-            const uint32_t g = div32(tm, a.div_s), in = tm - g * (uint32_t)s;
-            t.seq = b;
-            t.j = (int64_t)g + 1;
-            t.opens = in == 0 || place == 0;
-            t.carry = in != 0 && place == 0;
-            t.last = place + 1 == w.n;
-            t.out = i >= i_beg;
-            if (t.out && (t.last || in + 1 == (uint32_t)s)) {
-              t.prow = pool_row(a.p, b, t.j - 1);
-              if (t.prow < 0 && lane == 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
-            }
-          }
-        }
-      }
-      if (lane == 0) sm.tok[u] = t;
-    }
-    for (int k = tid; k < U * (KPT * NW / 4); k += NT) {
+    const int nu = i_end - r0 < U ? (int)(i_end - r0) : U;  // tokens of this round
+    for (int k = tid; k < nu * (KPT * NW / 4); k += NT) {
       const int u = k / (KPT * NW / 4), e = (k - u * (KPT * NW / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r0 + u < i_end && e < a.r) {
+      if (r0 + u >= 0 && e < a.r) {
         const T* src = reinterpret_cast<const T*>(a.m.c_new) + (r0 + u) * a.r + e;
-        v = make_float4(ld_f32(src), ld_f32(src + 1), ld_f32(src + 2), ld_f32(src + 3));
+        v = ld4(src);
       }
       *reinterpret_cast<float4*>(cs + u * (KPT * NW) + e) = v;
     }
+    if (warp == 0) {  // the round's tokens, a lane each
+      int b;
+      AppendWin w;
+      warp_windows(a, r0, b, w);
+      const int64_t i = r0 + lane, place = i - w.first;
+      Tok t;
+      t.seq = -1;
+      t.group = t.pos = 0;
+      t.opens = t.carry = t.last = t.row = 0;
+      if (lane < nu && i >= 0 && b >= 0 && place < w.n) {
+        t.seq = b;
+        t.pos = (uint32_t)(w.t0 + place);
+        t.group = div32(t.pos, a.div_s);
+        const uint32_t in = t.pos - t.group * (uint32_t)s;
+        t.opens = in == 0 || place == 0;
+        t.carry = in != 0 && place == 0;
+        t.last = place + 1 == w.n;
+        t.row = t.last || in + 1 == (uint32_t)s;
+      }
+      if (lane < U) sm.tok[lane] = t;
+    }
     __syncthreads();
+    // what this warp's two tokens need later, requested before the products
+    float pv[U / NW], tv[U / NW], xv[U / NW], yv[U / NW];
+    int32_t page[U / NW];
+#pragma unroll
+    for (int h = 0; h < U / NW; ++h) {
+      const int u = warp + h * NW;
+      const Tok t = sm.tok[u];
+      pv[h] = tv[h] = xv[h] = yv[h] = 0.f;
+      page[h] = -1;
+      if (t.seq >= 0) {
+        if (t.row && r0 + u >= i_beg)
+          page[h] = a.p.table[(int64_t)t.seq * a.p.table_pages + div32(t.group, a.p.div_rows)];
+        if (live) {
+          pv[h] = __ldg(a.m.P + (int64_t)t.group * D + ch);
+          if (t.carry) tv[h] = a.tail_in[(int64_t)t.seq * D + ch];
+          if (ch >= a.r) {
+            const T* kr = reinterpret_cast<const T*>(a.m.kR_new) + (r0 + u) * a.d_R;
+            xv[h] = ld_f32(kr + (ch - a.r));
+            if (a.rotate) yv[h] = ld_f32(kr + ((ch - a.r) ^ 1));
+          }
+        }
+      }
+    }
     {
       float acc[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) acc[u] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KPT; k += 4) {
+      for (int g = 0; g < U; g += 4) {
+        if (g < nu) {  // four tokens at a time: a few tokens do not pay for sixteen
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float4 c4 = *reinterpret_cast<const float4*>(cs + u * (KPT * NW) + warp * KPT + k);
-          acc[u] = fmaf(c4.x, wv[k], acc[u]);
-          acc[u] = fmaf(c4.y, wv[k + 1], acc[u]);
-          acc[u] = fmaf(c4.z, wv[k + 2], acc[u]);
-          acc[u] = fmaf(c4.w, wv[k + 3], acc[u]);
+          for (int k = 0; k < KPT; k += 4) {
+#pragma unroll
+            for (int u = g; u < g + 4; ++u) {
+              const float4 c4 = *reinterpret_cast<const float4*>(cs + u * (KPT * NW) + warp * KPT + k);
+              acc[u] = fmaf(c4.x, wv[k], acc[u]);
+              acc[u] = fmaf(c4.y, wv[k + 1], acc[u]);
+              acc[u] = fmaf(c4.z, wv[k + 2], acc[u]);
+              acc[u] = fmaf(c4.w, wv[k + 3], acc[u]);
+            }
+          }
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) sm.part[warp][u][lane] = acc[u];
+      for (int u = 0; u < U; ++u)
+        if (u < nu) sm.part[warp][u][lane] = acc[u];
     }
     __syncthreads();
-    for (int u = warp; u < U; u += NW) {  // gated entries
+#pragma unroll
+    for (int h = 0; h < U / NW; ++h) {  // gated entries
+      const int u = warp + h * NW;
       const Tok t = sm.tok[u];
       float e = 0.f;
       if (t.seq >= 0 && live) {
         float g = bc;
 #pragma unroll
         for (int w = 0; w < NW; ++w) g += sm.part[w][u][lane];
-        const int64_t i = r0 + u;
-        float x;
+        float x = xv[h];
         if (ch < a.r) {
           x = cs[u * (KPT * NW) + ch];
-        } else {
-          const T* kr = reinterpret_cast<const T*>(a.m.kR_new) + i * a.d_R;
+        } else if (a.rotate) {
           const int k = ch - a.r;
-          x = ld_f32(kr + k);
-          if (a.rotate) {
-            const float y = ld_f32(kr + (k ^ 1));
-            const AppendWin w = append_win(a, t.seq, false);
-            const float2 r = rope_cos_sin((uint32_t)(w.t0 + (i - w.first)), a.rope.turns[k >> 1]);
-            x = (k & 1) ? y * r.y + x * r.x : x * r.x - y * r.y;
-          }
+          const float2 r = rope_cos_sin(t.pos, a.rope.turns[k >> 1]);
+          x = (k & 1) ? yv[h] * r.y + x * r.x : x * r.x - yv[h] * r.y;
         }
-        e = x * sigmoidf_(g * __ldg(a.m.P + (t.j - 1) * D + ch));
+        e = tv[h] + x * sigmoidf_(g * pv[h]);
       }
       sm.v[u][lane] = e;
     }
@@ -205,22 +246,28 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
     if (warp == 0) {  // running sums, in token order
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const Tok t = sm.tok[u];
-        const float e = sm.v[u][lane];
-        if (t.seq >= 0) {
-          if (t.opens) run = t.carry && live ? a.tail_in[(int64_t)t.seq * D + ch] + e : e;
-          else run += e;
+        if (u < nu) {
+          run = (sm.tok[u].opens ? 0.f : run) + sm.v[u][lane];
+          sm.v[u][lane] = run;
         }
-        sm.v[u][lane] = run;
       }
     }
     __syncthreads();
-    for (int u = warp; u < U; u += NW) {
+#pragma unroll
+    for (int h = 0; h < U / NW; ++h) {
+      const int u = warp + h * NW;
       const Tok t = sm.tok[u];
-      if (t.seq < 0 || !t.out || !live) continue;
+      if (t.seq < 0 || r0 + u < i_beg || !live) continue;
       const float v = sm.v[u][lane];
       if (a.row_state) st_elem(reinterpret_cast<T*>(a.row_state) + (r0 + u) * D + ch, v);
-      if (t.prow >= 0) st_elem(reinterpret_cast<T*>(a.p.pages) + t.prow * a.p.row_stride + ch, v);
+      if (t.row) {
+        if (page[h] >= 0 && page[h] < a.p.num_pages) {
+          const int64_t row = (int64_t)page[h] * a.p.page_rows + (t.group - div32(t.group, a.p.div_rows) * a.p.page_rows);
+          st_elem(reinterpret_cast<T*>(a.p.pages) + row * a.p.row_stride + ch, v);
+        } else if (lane == 0) {
+          set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+        }
+      }
       if (t.last) a.tail_out[(int64_t)t.seq * D + ch] = v;
     }
     __syncthreads();
@@ -239,14 +286,21 @@ static auto pick(int r) -> void (*)(const PagedAppendArgs, int, int) {
 cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st) {
   const int D = a.r + a.d_R, slabs = (D + 31) / 32;
   // Tile length: one round of 16 tokens while that does not give every SM its
-  // eight blocks, then longer (W_c is read once a block); and not below the
-  // stride, up to 512 tokens, so that a tile recomputes at most about its own
-  // length again.
+  // eight blocks, then longer (W_c is read once a block).  A stride of up to 9
+  // takes the s - 1 rows before a tile into its rounds; with a longer one the
+  // tile is not below the stride, up to 512 tokens, so that it recomputes at
+  // most about its own length again.
   int64_t rounds = cdiv((int64_t)a.c.N * slabs, (int64_t)pap::U * sms * 8);
   rounds = rounds < 1 ? 1 : (rounds > 16 ? 16 : rounds);
   int64_t tt = rounds * pap::U;
-  const int64_t up = cdiv(a.s < 512 ? a.s : 512, pap::U) * pap::U;
-  if (tt < up) tt = up;
+  if (a.s <= 9) {
+    a.halo = a.s - 1;
+    tt -= a.halo;
+  } else {
+    a.halo = -1;
+    const int64_t up = cdiv(a.s < 512 ? a.s : 512, pap::U) * pap::U;
+    if (tt < up) tt = up;
+  }
   a.tt = (int)tt;
   const int kpt = a.r <= 64 ? 8 : (a.r <= 256 ? 32 : 64);
   const size_t smem = sizeof(pap::Smem) + (size_t)pap::U * kpt * pap::NW * 4;

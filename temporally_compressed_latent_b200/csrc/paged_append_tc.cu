@@ -105,28 +105,6 @@ __device__ __forceinline__ float gated(float v, float y) {
 }
 constexpr float kNegLog2e = -1.4426950408889634f;
 
-// The sequences of token rows base + lane + 32 m, m < NM (b[m] = -1: none).
-// A search for the first row, then the following starts 32 at a time.
-template <int NM>
-__device__ __forceinline__ void warp_sequences(const ChunkDev& c, int64_t base, int (&b)[NM]) {
-  const int lane = threadIdx.x & 31;
-  const int64_t first = base > 0 ? base : 0, last = base + 32 * NM - 1;
-  int b0 = warp_find_seq(c.tok_start, c.B, (int)(first < c.N ? first : c.N));
-#pragma unroll
-  for (int m = 0; m < NM; ++m) b[m] = b0;
-  for (int bb = b0 + 1; bb < c.B; bb += 32) {
-    const int v = bb + lane < c.B ? c.tok_start[bb + lane] : 0x7fffffff;
-    if (__shfl_sync(0xffffffffu, v, 0) > last) break;
-    for (int k = 0; k < 32; ++k) {
-      const int sk = __shfl_sync(0xffffffffu, v, k);
-      if (sk > last) break;
-#pragma unroll
-      for (int m = 0; m < NM; ++m)
-        if (sk <= base + lane + 32 * m) b[m] = bb + k;
-    }
-  }
-}
-
 // Rotates the queries: a warp takes QROWS token rows, all their loads in flight
 // before the first angle; a half of the warp computes a token's 16 angles, a
 // lane turns 16 bytes of a row.  It reads nothing that the append kernel

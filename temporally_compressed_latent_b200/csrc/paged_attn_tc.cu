@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  tc_fence_before();
   SeqWin* const wins = reinterpret_cast<SeqWin*>(sm + OFF_WIN);
+  tc_fence_before();
   plan_block<NT>(a.c, a.p, a.plan, gridDim.x, blockIdx.x, a.dev_err, plan, wins);  // (holds block barriers)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
@@ -211,31 +211,30 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     ItemWalk walk;
     walk.init(a.c, a.p, a.plan, blockIdx.x, plan, wins);
     SplitDesc desc = {0, 0, 0, 0, 0, 0};
-    uint32_t n = 0;
-    for (;; ++n) {
-      Item it;
-      const bool any = walk.next(a.c, a.p, a.plan, &it);
+    for (uint32_t n = 0;; ++n) {
+      Item item;
+      const bool any = walk.next(a.c, a.p, a.plan, &item);
       const int e = n % RING;
       if (n >= (uint32_t)RING && !warp_wait(&it_empty[e], ((n / RING) & 1) ^ 1)) { ok = false; break; }
       if (lane == 0) {
         RingItem r;
-        r.b = any ? it.b : 0;
-        r.row0 = any ? it.row0 : 0;
-        r.ntok = any ? it.ntok : 0;
-        r.R = any ? (int)it.R : 0;
-        r.t = any ? it.t : 0;
-        r.kt0 = any ? it.kt0 : 0;
-        r.kt1 = any ? it.kt1 : 0;
-        r.slot = any ? it.slot : -1;
+        r.b = any ? item.b : 0;
+        r.row0 = any ? item.row0 : 0;
+        r.ntok = any ? item.ntok : 0;
+        r.R = any ? (int)item.R : 0;
+        r.t = any ? item.t : 0;
+        r.kt0 = any ? item.kt0 : 0;
+        r.kt1 = any ? item.kt1 : 0;
+        r.slot = any ? item.slot : -1;
         r.pad = 0;
         ring[e] = r;
         mbar_arrive(&it_full[e]);
       }
       __syncwarp();
       if (!any) break;
-      if (it.slot >= 0 && it.kt1 == it.kt) {  // a split item ends in this block
-        desc.row0 = it.row0;
-        desc.ntok = it.ntok;
+      if (item.slot >= 0 && item.kt1 == item.kt) {  // a split item ends in this block
+        desc.row0 = item.row0;
+        desc.ntok = item.ntok;
         desc.first = first_block(a.plan, walk.C, walk.G, walk.item_start);
         desc.C = walk.C;
         desc.G = walk.G;
@@ -514,32 +513,38 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           for (int c = 0; c < 32; ++c) mq[c & 3] = fmaxf(mq[c & 3], x[c]);
           // (the scale is positive: the maximum of the scaled scores)
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
-          xmax[(xb * 2 + hf) * BM + i] = mx;
+          // the row's maximum grew by more than 2^8 in either half: agree on it and
+          // rescale l and, once the previous value MMA has landed, this half of
+          // the row of O (warp-collective); else nothing is exchanged
           tc_fence_before();
-          named_bar(1 + qw, 64);
+          const bool any = pair_or(1 + qw, on && mx > m_run + 8.f);
           tc_fence_after();
-          const float rmx = fmaxf(mx, xmax[(xb * 2 + (hf ^ 1)) * BM + i]);
-          const bool grow = on && rmx > m_run + 8.f;
-          const bool resc = grow && m_run != -INFINITY;
-          if (kt > it.kt0 && __any_sync(0xffffffffu, resc)) {
-            const uint32_t jp = kc - 1;
-            if (ok && !warp_wait(&p_empty[jp % NSB], (jp / NSB) & 1)) ok = false;
-            tc_fence_after();
-            const float f = resc ? exp2f(m_run - rmx) : 1.f;
+          if (any) {
+            xmax[(xb * 2 + hf) * BM + i] = mx;
+            named_bar(1 + qw, 64);
+            const float rmx = fmaxf(mx, xmax[(xb * 2 + (hf ^ 1)) * BM + i]);
+            const bool grow = on && rmx > m_run + 8.f;
+            const bool resc = grow && m_run != -INFINITY;
+            if (kt > it.kt0 && __any_sync(0xffffffffu, resc)) {
+              const uint32_t jp = kc - 1;
+              if (ok && !warp_wait(&p_empty[jp % NSB], (jp / NSB) & 1)) ok = false;
+              tc_fence_after();
+              const float f = resc ? exp2f(m_run - rmx) : 1.f;
 #pragma unroll 1
-            for (int ch = 0; ch < R / 64; ++ch) {
-              uint32_t ov[32];
-              const uint32_t col = O_COL + 128 * hf + 32 * ch;
-              tmem_ld32(lane_base + col, ov);
-              tmem_wait_ld();
+              for (int ch = 0; ch < R / 64; ++ch) {
+                uint32_t ov[32];
+                const uint32_t col = O_COL + 128 * hf + 32 * ch;
+                tmem_ld32(lane_base + col, ov);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-              tmem_st32(lane_base + col, ov);
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                tmem_st32(lane_base + col, ov);
+              }
+              tmem_wait_st();
+              l *= f;
             }
-            tmem_wait_st();
-            l *= f;
+            if (grow) m_run = rmx;
           }
-          if (grow) m_run = rmx;
           const float mref = m_run == -INFINITY ? 0.f : m_run;
           uint32_t pk[16];
           float lq[4] = {0.f, 0.f, 0.f, 0.f};
