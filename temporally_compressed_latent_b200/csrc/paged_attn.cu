@@ -13,9 +13,11 @@
 // so every row that is stored has at least one visible column.
 //
 // A block walks its share of the items (paged.cuh): 32 (token, head) rows of a
-// sequence against key tiles of 32 rows.  The scores take 2 x 2 per thread
-// from shared memory with float4 loads, the values 4 rows x 4 n channels per
-// thread with the running output in registers.  FFMA issue bounds it.
+// sequence against key tiles of 32 rows, which asynchronous copies bring two
+// tiles ahead (table entries one more).  The scores take 2 x 2 per thread from
+// shared memory with four-wide loads, the values 4 rows x 4 n channels per
+// thread with the running output in registers.  FFMA issue bounds it where a
+// chunk is long, the chain of a tile's steps where it is short.
 #include "paged.cuh"
 
 namespace mtla {
@@ -23,7 +25,10 @@ namespace psimt {
 
 constexpr int NT = 256;
 
-size_t smem_bytes(int D) { return (size_t)(PSM + PSN) * (D + 4) * 4 + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + sizeof(PlanShared) + NT * sizeof(SeqWin) + sizeof(Item) + 64; }
+// key rows in shared memory: 4 elements more than the row, so that reads of 16
+// rows touch every bank group once
+__host__ __device__ inline int key_pitch(int D, int elem) { return (D + 16 / elem) * elem; }
+size_t smem_bytes(int D, int elem) { return (size_t)PSM * (D + 4) * 4 + (size_t)2 * PSN * key_pitch(D, elem) + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + sizeof(PlanShared) + NT * sizeof(SeqWin) + sizeof(Item) + 64; }
 
 template <typename T> __device__ __forceinline__ void ld4(const T* p, float* v);
 template <> __device__ __forceinline__ void ld4<float>(const float* p, float* v) {
@@ -37,14 +42,20 @@ template <> __device__ __forceinline__ void ld4<__nv_bfloat16>(const __nv_bfloat
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
+template <typename T> __device__ __forceinline__ float4 ld4v(const T* p) {
+  float v[4];
+  ld4(p, v);
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // NQ: channel quads per lane, ceil(r / 128)
 template <typename T, int NQ>
 __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs a) {
   extern __shared__ float smem[];
-  const int D = a.r + a.d_R, DP = D + 4;  // row pitch: float4 reads of 16 rows touch every bank group once
+  const int D = a.r + a.d_R, DP = D + 4, KP = key_pitch(D, sizeof(T)), KT = KP / (int)sizeof(T);
   float* Qs = smem;                       // [PSM][DP]
-  float* Ks = Qs + PSM * DP;              // [PSN][DP]
-  float* Ss = Ks + PSN * DP;              // [PSN][PSM + 4]: probabilities, key-major
+  uint8_t* Kb = reinterpret_cast<uint8_t*>(Qs + PSM * DP);              // [2][PSN rows of KP bytes]
+  float* Ss = reinterpret_cast<float*>(Kb + 2 * PSN * KP);              // [PSN][PSM + 4]: probabilities, key-major
   float* sm_m = Ss + PSN * (PSM + 4);     // [PSM] running maxima
   float* sm_l = sm_m + PSM;               // [PSM] running sums
   float* sm_a = sm_l + PSM;               // [PSM] rescale factors of the current tile
@@ -105,21 +116,46 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
 #pragma unroll
       for (int c = 0; c < NQ * 4; ++c) o[i][c] = 0.f;
 
+    // keys: cache rows, then the tokens' own states; rows between and behind
+    // them are zeros.  A warp brings rows warp, warp + 8, ... of a tile; lane l
+    // of it looks up row (l mod 4)'s page a tile ahead.
+    constexpr int RW = PSN / (NT / 32);           // rows a warp (4)
+    const int chunks = D * (int)sizeof(T) / 16;   // 16-byte pieces of a row
+    auto look = [&](int kt) -> int64_t {          // pool row, -1: zeros, or -2 - token: an own state
+      const int64_t g = (int64_t)kt * PSN + warp + (lane % RW) * (NT / 32);
+      if (g < it.R) {
+        const int64_t row = pool_row(a.p, it.b, g);
+        if (row < 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
+        return row;
+      }
+      return g >= R8 && g - R8 < it.ntok ? -2 - (it.row0 + (g - R8)) : -1;
+    };
+    auto copy = [&](int64_t at, int buf) {
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        const int64_t row = __shfl_sync(0xffffffffu, at, k);
+        const T* src = row >= 0 ? reinterpret_cast<const T*>(a.p.pages) + row * a.p.row_stride
+                                : reinterpret_cast<const T*>(a.row_state) + (row == -1 ? 0 : -2 - row) * D;
+        const uint32_t dst = smem_u32(Kb + (buf * PSN + warp + k * (NT / 32)) * KP);
+        const int bytes = row == -1 ? 0 : 16;     // (0: the piece is filled with zeros)
+        for (int c = lane; c < chunks; c += 32)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16),
+                       "l"(reinterpret_cast<const uint8_t*>(src) + c * 16), "r"(bytes) : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy(look(it.kt0), 0);
+    int64_t ahead = it.kt0 + 1 < it.kt1 ? look(it.kt0 + 1) : -1;
+
     for (int kt = it.kt0; kt < it.kt1; ++kt) {
-      const int64_t v0 = (int64_t)kt * PSN;  // first virtual row
-      // keys: cache rows, then the tokens' own states; rows between and behind them are zeros
-      for (int k = tid; k < PSN * (D / 4); k += NT) {
-        const int i = k / (D / 4), e = (k - i * (D / 4)) * 4;
-        const int64_t g = v0 + i;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (g < it.R) {
-          const int64_t pr = pool_row(a.p, it.b, g);
-          if (pr >= 0) ld4(reinterpret_cast<const T*>(a.p.pages) + pr * a.p.row_stride + e, v);
-          else if (e == 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
-        } else if (g >= R8 && g - R8 < it.ntok) {
-          ld4(reinterpret_cast<const T*>(a.row_state) + (it.row0 + (g - R8)) * D + e, v);
-        }
-        *reinterpret_cast<float4*>(Ks + i * DP + e) = make_float4(v[0], v[1], v[2], v[3]);
+      const int64_t v0 = (int64_t)kt * PSN;       // first virtual row
+      const T* Ks = reinterpret_cast<const T*>(Kb + ((kt - it.kt0) & 1) * PSN * KP);
+      if (kt + 1 < it.kt1) {
+        copy(ahead, (kt + 1 - it.kt0) & 1);
+        ahead = kt + 2 < it.kt1 ? look(kt + 2) : -1;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       __syncthreads();
       // scores: rows r0, r0 + 16; keys c0, c0 + 16
@@ -128,8 +164,8 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       for (int e = 0; e < D; e += 4) {
         const float4 q0 = *reinterpret_cast<const float4*>(Qs + r0 * DP + e);
         const float4 q1 = *reinterpret_cast<const float4*>(Qs + (r0 + 16) * DP + e);
-        const float4 k0 = *reinterpret_cast<const float4*>(Ks + c0 * DP + e);
-        const float4 k1 = *reinterpret_cast<const float4*>(Ks + (c0 + 16) * DP + e);
+        const float4 k0 = ld4v(Ks + c0 * KT + e);
+        const float4 k1 = ld4v(Ks + (c0 + 16) * KT + e);
         s00 = fmaf(q0.x, k0.x, s00); s00 = fmaf(q0.y, k0.y, s00); s00 = fmaf(q0.z, k0.z, s00); s00 = fmaf(q0.w, k0.w, s00);
         s01 = fmaf(q0.x, k1.x, s01); s01 = fmaf(q0.y, k1.y, s01); s01 = fmaf(q0.z, k1.z, s01); s01 = fmaf(q0.w, k1.w, s01);
         s10 = fmaf(q1.x, k0.x, s10); s10 = fmaf(q1.y, k0.y, s10); s10 = fmaf(q1.z, k0.z, s10); s10 = fmaf(q1.w, k0.w, s10);
@@ -191,7 +227,7 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
           for (int q = 0; q < NQ; ++q) {
             const int e = 4 * lane + 128 * q;
             if (e < a.r) {
-              const float4 c4 = *reinterpret_cast<const float4*>(Ks + k * DP + e);
+              const float4 c4 = ld4v(Ks + k * KT + e);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 o[i][4 * q] = fmaf(pv[i], c4.x, o[i][4 * q]);
@@ -370,9 +406,9 @@ int paged_simt_grid(int r, int d_R, int dtype, int sms) {
   if (last.dev == dev && last.r == r && last.d_R == d_R && last.dtype == dtype) return last.grid;
   auto k = dtype == MTLA_BF16 ? psimt::simt_kernel<__nv_bfloat16>(r) : psimt::simt_kernel<float>(r);
   int occ = 0;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psimt::smem_bytes(576)) != cudaSuccess)
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psimt::smem_bytes(576, dtype == MTLA_BF16 ? 2 : 4)) != cudaSuccess)
     return 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, psimt::smem_bytes(r + d_R)) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, psimt::smem_bytes(r + d_R, dtype == MTLA_BF16 ? 2 : 4)) != cudaSuccess ||
       occ < 1)
     return 0;
   last.dev = dev;
@@ -391,7 +427,7 @@ cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(psimt::NT);
-  cfg.dynamicSmemBytes = psimt::smem_bytes(a.r + a.d_R);
+  cfg.dynamicSmemBytes = psimt::smem_bytes(a.r + a.d_R, dtype == MTLA_BF16 ? 2 : 4);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -156,21 +156,21 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
   int round = 0;
   for (;; ++round) {
     double sum = 0.0;
-    // two runs at a time: up to 32 loads of a lane in flight
-    for (int r = warp; r < mine; r += 2 * NW) {
-      float pa[2][8], qa[2][8];
+    // the next run's loads are in flight while one is summed
+    float pa[8], qa[8], pb[8], qb[8];
+    if (warp < mine) w.load((r_beg + warp) * RUN, pa, qa);
+    for (int r = warp; r < mine; r += NW) {
+      if (r + NW < mine) w.load((r_beg + r + NW) * RUN, pb, qb);
+      double x[8];
+      w.weigh((r_beg + r) * RUN, pa, qa, x);
+      const double s = warp_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+      if (lane == 0) run_sum[r] = s;
+      sum += s;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (r + h * NW < mine) w.load((r_beg + r + h * NW) * RUN, pa[h], qa[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (r + h * NW < mine) {
-          double x[8];
-          w.weigh((r_beg + r + h * NW) * RUN, pa[h], qa[h], x);
-          const double s = warp_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
-          if (lane == 0) run_sum[r + h * NW] = s;
-          sum += s;
-        }
+      for (int k = 0; k < 8; ++k) {
+        pa[k] = pb[k];
+        qa[k] = qb[k];
+      }
     }
     if (lane == 0) warp_total[warp] = sum;
     if (round == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
