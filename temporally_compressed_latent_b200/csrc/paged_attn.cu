@@ -16,8 +16,10 @@
 // sequence against key tiles of 32 rows, which asynchronous copies bring two
 // tiles ahead (table entries one more).  The scores take 2 x 2 per thread from
 // shared memory with four-wide loads, the values 4 rows x 4 n channels per
-// thread with the running output in registers.  FFMA issue bounds it where a
-// chunk is long, the chain of a tile's steps where it is short.
+// thread with the running output in registers, two products an instruction
+// (packed fp32); rows of up to 64 latents leave half of a warp's lanes to take
+// the tile's other keys.  Issue bounds it where a chunk is long, the chain of a
+// tile's steps where it is short.
 #include "paged.cuh"
 
 namespace mtla {
@@ -48,9 +50,34 @@ template <typename T> __device__ __forceinline__ float4 ld4v(const T* p) {
   return make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// NQ: channel quads per lane, ceil(r / 128)
-template <typename T, int NQ>
+// two fp32 products and sums in one instruction
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// NQ: channel quads per lane, ceil(r / 128); 0: r <= 64, where lanes 16 .. 31
+// take every second key
+template <typename T, int NQ0>
 __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs a) {
+  constexpr int NQ = NQ0 > 0 ? NQ0 : 1, NK = NQ0 > 0 ? 1 : 2;  // channel quads; key groups of a warp
+  const int kg = NK == 2 ? (int)(threadIdx.x & 31) >> 4 : 0, cl = NK == 2 ? (int)threadIdx.x & 15 : (int)threadIdx.x & 31;
   extern __shared__ float smem[];
   const int D = a.r + a.d_R, DP = D + 4, KP = key_pitch(D, sizeof(T)), KT = KP / (int)sizeof(T);
   float* Qs = smem;                       // [PSM][DP]
@@ -110,11 +137,11 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       sm_m[tid] = -INFINITY;
       sm_l[tid] = 0.f;
     }
-    float o[4][NQ * 4];
+    uint64_t o[4][NQ * 2];                       // rows 4 warp + i, channel pairs
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < NQ * 4; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < NQ * 2; ++c) o[i][c] = 0;
 
     // keys: cache rows, then the tokens' own states; rows between and behind
     // them are zeros.  A warp brings rows warp, warp + 8, ... of a tile; lane l
@@ -160,17 +187,20 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       __syncthreads();
       // scores: rows r0, r0 + 16; keys c0, c0 + 16
       const int r0 = tid >> 4, c0 = tid & 15;
-      float s00 = 0.f, s01 = 0.f, s10 = 0.f, s11 = 0.f;
+      uint64_t t00 = 0, t01 = 0, t10 = 0, t11 = 0;
+#pragma unroll 2
       for (int e = 0; e < D; e += 4) {
-        const float4 q0 = *reinterpret_cast<const float4*>(Qs + r0 * DP + e);
-        const float4 q1 = *reinterpret_cast<const float4*>(Qs + (r0 + 16) * DP + e);
-        const float4 k0 = ld4v(Ks + c0 * KT + e);
-        const float4 k1 = ld4v(Ks + (c0 + 16) * KT + e);
-        s00 = fmaf(q0.x, k0.x, s00); s00 = fmaf(q0.y, k0.y, s00); s00 = fmaf(q0.z, k0.z, s00); s00 = fmaf(q0.w, k0.w, s00);
-        s01 = fmaf(q0.x, k1.x, s01); s01 = fmaf(q0.y, k1.y, s01); s01 = fmaf(q0.z, k1.z, s01); s01 = fmaf(q0.w, k1.w, s01);
-        s10 = fmaf(q1.x, k0.x, s10); s10 = fmaf(q1.y, k0.y, s10); s10 = fmaf(q1.z, k0.z, s10); s10 = fmaf(q1.w, k0.w, s10);
-        s11 = fmaf(q1.x, k1.x, s11); s11 = fmaf(q1.y, k1.y, s11); s11 = fmaf(q1.z, k1.z, s11); s11 = fmaf(q1.w, k1.w, s11);
+        const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(Qs + r0 * DP + e);
+        const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(Qs + (r0 + 16) * DP + e);
+        const float4 f0 = ld4v(Ks + c0 * KT + e), f1 = ld4v(Ks + (c0 + 16) * KT + e);
+        const uint64_t k0x = pack2(f0.x, f0.y), k0y = pack2(f0.z, f0.w), k1x = pack2(f1.x, f1.y), k1y = pack2(f1.z, f1.w);
+        t00 = fma2(q0.y, k0y, fma2(q0.x, k0x, t00));
+        t01 = fma2(q0.y, k1y, fma2(q0.x, k1x, t01));
+        t10 = fma2(q1.y, k0y, fma2(q1.x, k0x, t10));
+        t11 = fma2(q1.y, k1y, fma2(q1.x, k1x, t11));
       }
+      auto both = [](uint64_t v) { const float2 f = unpack2(v); return f.x + f.y; };
+      const float s00 = both(t00), s01 = both(t01), s10 = both(t10), s11 = both(t11);
       auto put = [&](int i, int c, float v) {
         const int tok = i / a.H;
         const int64_t g = v0 + c, seen = rows_below(a.plan, it.t + tok);
@@ -211,29 +241,28 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
         }
       }
       __syncthreads();
-      // values: this warp's rows 4 warp .. + 3, channels 4 lane + 128 q
+      // values: this warp's rows 4 warp .. + 3, channels 4 cl + 128 q
       if (4 * warp < live) {
         const float4 f = *reinterpret_cast<const float4*>(sm_a + 4 * warp);
-        const float fa[4] = {f.x, f.y, f.z, f.w};
+        const uint64_t fa[4] = {pack2(f.x, f.x), pack2(f.y, f.y), pack2(f.z, f.z), pack2(f.w, f.w)};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int c = 0; c < NQ * 4; ++c) o[i][c] *= fa[i];
+          for (int c = 0; c < NQ * 2; ++c) o[i][c] = mul2(o[i][c], fa[i]);
 #pragma unroll 4
-        for (int k = 0; k < PSN; ++k) {
+        for (int k = kg; k < PSN; k += NK) {
           const float4 p4 = *reinterpret_cast<const float4*>(Ss + k * (PSM + 4) + 4 * warp);
-          const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
+          const uint64_t pv[4] = {pack2(p4.x, p4.x), pack2(p4.y, p4.y), pack2(p4.z, p4.z), pack2(p4.w, p4.w)};
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            const int e = 4 * lane + 128 * q;
+            const int e = 4 * cl + 128 * q;
             if (e < a.r) {
               const float4 c4 = ld4v(Ks + k * KT + e);
+              const uint64_t cx = pack2(c4.x, c4.y), cy = pack2(c4.z, c4.w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                o[i][4 * q] = fmaf(pv[i], c4.x, o[i][4 * q]);
-                o[i][4 * q + 1] = fmaf(pv[i], c4.y, o[i][4 * q + 1]);
-                o[i][4 * q + 2] = fmaf(pv[i], c4.z, o[i][4 * q + 2]);
-                o[i][4 * q + 3] = fmaf(pv[i], c4.w, o[i][4 * q + 3]);
+                o[i][2 * q] = fma2(pv[i], cx, o[i][2 * q]);
+                o[i][2 * q + 1] = fma2(pv[i], cy, o[i][2 * q + 1]);
               }
             }
           }
@@ -241,37 +270,38 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       }
       __syncthreads();
     }
+    if (NK == 2) {  // the two key groups' sums
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NQ * 2; ++c) {
+          const float2 v = unpack2(o[i][c]);
+          o[i][c] = pack2(v.x + __shfl_xor_sync(0xffffffffu, v.x, 16), v.y + __shfl_xor_sync(0xffffffffu, v.y, 16));
+        }
+    }
     // the item's rows out: finished, or as a part
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * warp + i;
-      if (row < live) {
+      if (row < live && kg == 0) {
         const float m = sm_m[row], l = sm_l[row];
-        if (it.slot < 0) {
-          const int64_t orow = (int64_t)it.row0 * a.H + row;
-          const float inv = 1.f / l;
-          if (a.lse && lane == 0) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+        const int64_t orow = (int64_t)it.row0 * a.H + row, prow = (int64_t)it.slot * a.rows + row;
+        const float inv = it.slot < 0 ? 1.f / l : 1.f;
+        if (lane == 0) {
+          if (it.slot >= 0) a.part.ml[prow] = make_float2(m, l);
+          else if (a.lse) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+        }
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const int e = 4 * lane + 128 * q;
-            if (e < a.r) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float v = o[i][4 * q + c] * inv;
-                if (a.out_f32) reinterpret_cast<float*>(a.out)[orow * a.r + e + c] = v;
-                else st_elem(reinterpret_cast<T*>(a.out) + orow * a.r + e + c, v);
-              }
-            }
-          }
-        } else {
-          const int64_t prow = (int64_t)it.slot * a.rows + row;
-          if (lane == 0) a.part.ml[prow] = make_float2(m, l);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const int e = 4 * lane + 128 * q;
-            if (e < a.r)
-              *reinterpret_cast<float4*>(a.part.o + prow * a.r + e) =
-                  make_float4(o[i][4 * q], o[i][4 * q + 1], o[i][4 * q + 2], o[i][4 * q + 3]);
+        for (int q = 0; q < NQ; ++q) {
+          const int e = 4 * cl + 128 * q;
+          if (e < a.r) {
+            const float2 x = unpack2(o[i][2 * q]), y = unpack2(o[i][2 * q + 1]);
+            const float4 v = make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+            if (it.slot >= 0) *reinterpret_cast<float4*>(a.part.o + prow * a.r + e) = v;
+            else if (a.out_f32 || sizeof(T) == 4) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.r + e) = v;
+            else
+              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * a.r + e) =
+                  make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
           }
         }
       }
@@ -387,6 +417,7 @@ __global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_cons
 
 template <typename T>
 static auto simt_kernel(int r) -> void (*)(const PagedAttnArgs) {
+  if (r <= 64) return paged_attn_simt_kernel<T, 0>;
   if (r <= 128) return paged_attn_simt_kernel<T, 1>;
   if (r <= 256) return paged_attn_simt_kernel<T, 2>;
   return paged_attn_simt_kernel<T, 4>;
