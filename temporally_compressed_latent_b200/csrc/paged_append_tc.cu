@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(QT, 4) paged_rotate_kernel(const __grid_consta
 __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ PagedAppendMaps mp,
                                                                 const __grid_constant__ PagedAppendArgs a, int n_tiles) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not an integer address: the compiler keeps seeing shared memory)
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   uint64_t* const k_full = bar;                  // [KS]
   uint64_t* const k_empty = bar + KS;            // [2] a tile's stages (epilogue)

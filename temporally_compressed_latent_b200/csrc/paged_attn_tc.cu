@@ -120,7 +120,8 @@ __device__ __forceinline__ int tile_groups(int R8g, int ntok, int kt) {
 __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnMaps mp,
                                                               const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not an integer address: the compiler keeps seeing shared memory)
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   uint64_t* const q_full = bar;
   uint64_t* const q_empty = bar + 1;            // the item's last score MMA has read Q
