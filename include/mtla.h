@@ -475,8 +475,8 @@ typedef struct {
  * sequence's tokens are cut into chunks does not change the sums: the open
  * group's sum travels in fp32.
  * A sequence whose chunk does not fit (ceil((t_prev + tokens)/s) above
- * table_pages * page_rows: MTLA_DEVERR_CAPACITY, as for t_prev < 0; above
- * J_max: MTLA_DEVERR_PE_RANGE) takes none of its tokens.
+ * table_pages * page_rows: MTLA_DEVERR_CAPACITY, as for times outside [0, 2^31);
+ * above J_max: MTLA_DEVERR_PE_RANGE) takes none of its tokens.
  *   workspace: mtla_paged_workspace_bytes(dims, B, N, MTLA_PAGED_APPEND) (0
  *   bytes today; NULL is fine then).
  * d_R even where anything is rotated (MTLA_ERR_UNSUPPORTED otherwise).
@@ -501,7 +501,7 @@ mtla_status mtla_paged_append(const mtla_dims *dims, int32_t B, const mtla_chunk
  *   q_abs [N, H, r], q_rope [N, H, d_R] (RoPE applied), row_state [N, D]: cache
  *   dtype; out [N, H, r] in out_dtype (the cache dtype, or MTLA_F32); lse
  *   [N, H] fp32 (nullable).
- * A sequence whose rows exceed its table (or with t_prev < 0) sets
+ * A sequence whose rows exceed its table (or times leave [0, 2^31)) sets
  * MTLA_DEVERR_CAPACITY and its rows of out and lse are left as they were.
  *   workspace: mtla_paged_workspace_bytes(dims, B, N, MTLA_PAGED_ATTN) bytes; no
  *   initialisation; for calls that run one after another.

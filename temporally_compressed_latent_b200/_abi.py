@@ -291,26 +291,37 @@ def mtla_paged_workspace_bytes(d, B, N, which) -> int:
     return int(lib.mtla_paged_workspace_bytes(_c.byref(d), B, N, which))
 
 
+def _paged_stream(stream, dev_err):
+    """The stream of a paged call.  Launches go to the current device: tensors of another one are refused
+    (a stream given by the caller is taken as it is)."""
+    if stream is None and not isinstance(dev_err, int):
+        import torch
+        if dev_err.get_device() != torch.cuda.current_device():
+            raise ValueError(f"the call's tensors are on {dev_err.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
 def mtla_paged_append(d, B, chunk, merge, rope_base, q_rope, q_rope_out, cache, tail_in, tail_out, t_out, cache_len,
                       row_state, workspace, workspace_bytes, dev_err, stream=None):
     _check(lib.mtla_paged_append(_c.byref(d), B, _c.byref(chunk), _c.byref(merge), rope_base, _ptr(q_rope),
                                  _ptr(q_rope_out), _c.byref(cache), _ptr(tail_in), _ptr(tail_out), _ptr(t_out),
                                  _ptr(cache_len), _ptr(row_state), _ptr(workspace), workspace_bytes, _ptr(dev_err),
-                                 _stream(stream)), "mtla_paged_append")
+                                 _paged_stream(stream, dev_err)), "mtla_paged_append")
 
 
 def mtla_paged_attn(d, B, chunk, q_abs, q_rope, row_state, cache, out, out_dtype, lse, workspace, workspace_bytes,
                     dev_err, stream=None):
     _check(lib.mtla_paged_attn(_c.byref(d), B, _c.byref(chunk), _ptr(q_abs), _ptr(q_rope), _ptr(row_state),
                                _c.byref(cache), _ptr(out), out_dtype, _ptr(lse), _ptr(workspace), workspace_bytes,
-                               _ptr(dev_err), _stream(stream)), "mtla_paged_attn")
+                               _ptr(dev_err), _paged_stream(stream, dev_err)), "mtla_paged_attn")
 
 
 def mtla_verify_drafts(B, N, V, p, ld_p, q, ld_q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err,
                        stream=None):
     _check(lib.mtla_verify_drafts(B, N, V, _ptr(p), ld_p, _ptr(q), ld_q, _ptr(tokens), _ptr(tok_start),
                                   _ptr(u_accept), _ptr(u_sample), _ptr(n_keep), _ptr(next_token), _ptr(dev_err),
-                                  _stream(stream)), "mtla_verify_drafts")
+                                  _paged_stream(stream, dev_err)), "mtla_verify_drafts")
 
 
 def mtla_workspace_bytes(d, B, which=WS_DECODE) -> int:

@@ -244,11 +244,11 @@ struct PlanShared {
 };
 
 // The chunk window the attention takes (a sequence whose rows exceed its table,
-// or with a negative time, takes none).
+// or whose times leave [0, 2^31), takes none).
 __device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p, const FastDiv& div_s, int b,
                                            int32_t* dev_err) {
   SeqWin w = seq_win(c, b);
-  if (w.n > 0 && (w.t0 < 0 || (int64_t)div32((uint32_t)(w.t0 + w.n - 1), div_s) > table_rows(p))) {
+  if (w.n > 0 && (w.t0 < 0 || w.t0 + w.n > 0x7fffffff || (int64_t)div32((uint32_t)(w.t0 + w.n - 1), div_s) > table_rows(p))) {
     if (dev_err) set_err(dev_err, MTLA_DEVERR_CAPACITY);
     w.n = 0;
   }
@@ -513,13 +513,13 @@ struct PagedAppendArgs {
   int halo;    // token rows before a tile that its block always computes too, or -1: as many as its first group needs
 };
 // The chunk window the append takes: a sequence that does not fit its table or
-// the P table (or has a negative time) takes none.  Times of a chunk are below
-// 2^32, so divisions by s are 32-bit.
+// the P table (or whose times leave [0, 2^31)) takes none.  Divisions by s are
+// 32-bit.
 using AppendWin = SeqWin;
 __device__ __forceinline__ void append_fit(const PagedAppendArgs& a, AppendWin& w, bool report) {
   if (w.n > 0) {
     const uint32_t j = div32((uint32_t)w.t0 + (uint32_t)w.n - 1u, a.div_s) + 1u;  // (of a t0 >= 0)
-    const bool cap = w.t0 < 0 || j > table_rows(a.p), pe = !cap && j > (uint32_t)a.m.J_max;
+    const bool cap = w.t0 < 0 || w.t0 + w.n > 0x7fffffff || j > table_rows(a.p), pe = !cap && j > (uint32_t)a.m.J_max;
     if (cap || pe) {
       if (report) set_err(a.dev_err, cap ? MTLA_DEVERR_CAPACITY : MTLA_DEVERR_PE_RANGE);
       w.n = 0;

@@ -130,15 +130,16 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   if (st != MTLA_OK) return st;
   PagedAppendArgs a;
   if ((st = chunk_args(B, chunk, &a.c)) != MTLA_OK || (st = cache_args(dims, cache, &a.p)) != MTLA_OK) return st;
-  if (!merge || !merge->c_new || !merge->kR_new || !merge->W_c || !merge->b_c || !merge->P || merge->J_max < 1)
-    return MTLA_ERR_INVALID_ARG;
+  if (!merge || !merge->W_c || !merge->b_c || !merge->P || merge->J_max < 1) return MTLA_ERR_INVALID_ARG;
+  // (arrays without rows or columns may be null)
+  if (chunk->N > 0 && (!merge->c_new || (!merge->kR_new && dims->d_R > 0))) return MTLA_ERR_INVALID_ARG;
   const void* ptrs[] = {merge->c_new, merge->kR_new, merge->W_c, merge->b_c, merge->P, row_state, q_rope, q_rope_out};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return MTLA_ERR_INVALID_ARG;
   if (!tail_in || !tail_out || !t_out || !dev_err || !aligned(tail_in, 4) || !aligned(tail_out, 4) ||
       !aligned(t_out, 4) || !aligned(cache_len, 4) || !aligned(dev_err, 4))
     return MTLA_ERR_INVALID_ARG;
-  if ((q_rope == nullptr) != (q_rope_out == nullptr)) return MTLA_ERR_INVALID_ARG;
+  if (chunk->N > 0 && dims->d_R > 0 && (q_rope == nullptr) != (q_rope_out == nullptr)) return MTLA_ERR_INVALID_ARG;
   if (!(rope_base == 0.0 || (rope_base > 0.0 && isfinite(rope_base)))) return MTLA_ERR_INVALID_ARG;
   if (rope_base > 0.0 && dims->d_R % 2) return MTLA_ERR_UNSUPPORTED;
   const size_t D = dims->r + dims->d_R;
@@ -156,7 +157,7 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
   a.m.J_max = merge->J_max;
   a.rotate = rope_base > 0.0 && dims->d_R > 0;
   if (a.rotate) rope_table(rope_base, dims->d_R, &a.rope);
-  a.q_rope = dims->d_R > 0 ? q_rope : nullptr;
+  a.q_rope = chunk->N > 0 && dims->d_R > 0 ? q_rope : nullptr;
   a.q_rope_out = q_rope_out;
   a.tail_in = tail_in;
   a.tail_out = tail_out;
@@ -192,7 +193,8 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   if (st != MTLA_OK) return st;
   PagedAttnArgs a;
   if ((st = chunk_args(B, chunk, &a.c)) != MTLA_OK || (st = cache_args(dims, cache, &a.p)) != MTLA_OK) return st;
-  if (!q_abs || (!q_rope && dims->d_R > 0) || !row_state || !out || !dev_err) return MTLA_ERR_INVALID_ARG;
+  if (!dev_err) return MTLA_ERR_INVALID_ARG;
+  if (chunk->N > 0 && (!q_abs || (!q_rope && dims->d_R > 0) || !row_state || !out)) return MTLA_ERR_INVALID_ARG;
   const void* ptrs[] = {q_abs, q_rope, row_state, out};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return MTLA_ERR_INVALID_ARG;
@@ -243,8 +245,8 @@ mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, 
                                const float* u_sample, int32_t* n_keep, int32_t* next_token, int32_t* dev_err,
                                void* stream) {
   if (B < 0 || N < 0 || V < 1 || V > (1 << 22) || ld_p < V || (q && ld_q < V)) return MTLA_ERR_INVALID_ARG;
-  if (!p || !tokens || !tok_start || !u_accept || !u_sample || !n_keep || !next_token || !dev_err)
-    return MTLA_ERR_INVALID_ARG;
+  if (!tok_start || !u_sample || !n_keep || !next_token || !dev_err) return MTLA_ERR_INVALID_ARG;
+  if (N > 0 && (!p || !tokens || !u_accept)) return MTLA_ERR_INVALID_ARG;
   const void* ptrs[] = {p, q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err};
   for (const void* x : ptrs)
     if (!aligned(x, 4)) return MTLA_ERR_INVALID_ARG;

@@ -26,6 +26,8 @@ def f64(t):
 def rotate(x, pos):
     """Channel pairs of x [..., d_R] turned by pos base^(-2k/d_R)."""
     d = x.shape[-1]
+    if d == 0:
+        return x
     ang = pos * BASE ** (-2.0 * np.arange(d // 2) / d)
     out = np.empty_like(x)
     out[..., 0::2] = x[..., 0::2] * np.cos(ang) - x[..., 1::2] * np.sin(ang)

@@ -85,6 +85,7 @@ def test_append_refusals():
     assert _append(t_out=P + 4) == INVALID and _append(clen=P) == INVALID
     # no sequences: nothing to do
     assert _append(B=0, chunk=_chunk(N=0)) == 0
+    assert _append(B=0, chunk=_chunk(N=0), c=None, q=None, qo=None, state=None) == 0
 
 
 def test_attn_refusals():
@@ -93,6 +94,7 @@ def test_attn_refusals():
     assert _attn(od=2) == INVALID
     assert _attn(d=_dims(dtype="f32"), cache=_cache(), od=1) == INVALID
     assert _attn(B=0) == 0 and _attn(chunk=_chunk(N=0)) == 0
+    assert _attn(chunk=_chunk(N=0), qa=None, qr=None, state=None, out=None, lse=None, ws=None) == 0
 
 
 def test_verify_refusals():
@@ -104,7 +106,7 @@ def test_verify_refusals():
     for name in ("p", "tok", "start", "ua", "us", "keep", "nxt", "err"):
         assert call(**{name: None}) == INVALID
         assert call(**{name: P + 2}) == INVALID
-    assert call(B=0) == 0
+    assert call(B=0) == 0 and call(B=0, N=0, p=None, tok=None, ua=None) == 0
 
 
 def test_workspace_query_needs_sound_arguments():
@@ -112,6 +114,14 @@ def test_workspace_query_needs_sound_arguments():
     assert mtla.mtla_paged_workspace_bytes(_dims(), 0, 1, mtla.PAGED_ATTN) == 0
     assert mtla.mtla_paged_workspace_bytes(_dims(), 1, 1, 9) == 0
     assert mtla.mtla_paged_workspace_bytes(_dims(), 1, 1, mtla.PAGED_APPEND) == 0
+
+
+def test_binding_refuses_tensors_of_another_device():
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("without a GPU there is no current device to compare with")
+    with pytest.raises(Exception):
+        mtla.mtla_verify_drafts(1, 3, 10, P, 10, P, 10, P, P, P, P, P, P, torch.zeros(1, dtype=torch.int32))
 
 
 def test_binding_raises_on_error_status():

@@ -81,6 +81,26 @@ def test_append_options(dims):
     b.check_append(b.append(rope_base=0.0, state=False), rope_base=0.0)
 
 
+@pytest.mark.parametrize("dims", [{}, TINY], ids=["main", "tiny"])
+def test_append_without_tokens(dims):
+    """Nothing new anywhere: times and tails are handed on; token arrays may have no rows at all."""
+    for spare in (2, 0):
+        b = Batch([0, 0, 0], [5, 0, 4], s=2, page_rows=8, spare_tokens=spare, seed=2, **dims)
+        b.check_append(b.append())
+        b.fill_groups()
+        b.check_attn(b.attn())
+        assert int(b.err.item()) == 0
+
+
+def test_without_rope_channels():
+    """d_R = 0: latents alone, no RoPE keys or queries."""
+    b = Batch([3, 0, 20, 1], [4, 9, 70, 0], dtype="f32", H=3, d_h=8, r=32, d_R=0, s=3, page_rows=8, seed=6)
+    b.check_append(b.append(q=False))
+    b = Batch([3, 0, 20, 1], [4, 9, 70, 0], dtype="f32", H=3, d_h=8, r=32, d_R=0, s=3, page_rows=8, seed=6)
+    b.fill_groups()
+    b.check_attn(b.attn())
+
+
 def test_append_far_position():
     """Angles at large times: the table of P limits a sequence's groups, so a large stride gives large times."""
     s = 1 << 20
@@ -152,6 +172,12 @@ def test_append_refuses_on_the_device(more):
     o = b.append()
     torch.cuda.synchronize()
     assert int(b.err.item()) == mtla.DEVERR_CAPACITY and o["t"].tolist() == [7, 33, -1, 8] + t_more
+    # a time past the 32-bit integers
+    b = Batch(new, past, s=s, page_rows=8, seed=8)
+    b.t_prev[3] = (1 << 31) - 3
+    o = b.append()
+    torch.cuda.synchronize()
+    assert int(b.err.item()) == mtla.DEVERR_CAPACITY and o["t"].tolist() == [7, 33, 5, (1 << 31) - 3] + t_more
     # a table entry outside the pool: its rows are not written, the rest is
     for bad in (-1, 1 << 30):
         b = Batch(new, past, s=s, page_rows=8, seed=8)
