@@ -347,16 +347,22 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
       if (lane == 0) mbar_arrive(&meta_full[mb]);
     }
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
-    if (warp == META_WARP1)                      // per-sequence results
-      for (int b = blockIdx.x; b < a.c.B; b += gridDim.x) {
-        const AppendWin w = append_win(a, b, lane == 0);
-        if (lane == 0) {
+    if (warp == META_WARP1)                      // per-sequence results, a lane each
+      for (int b0 = blockIdx.x * 32; b0 < a.c.B; b0 += gridDim.x * 32) {
+        const int b = b0 + lane;
+        bool copy = false;
+        if (b < a.c.B) {
+          const AppendWin w = append_win(a, b, true);
           a.t_out[b] = (int32_t)(w.t0 + w.n);
           if (a.cache_len) a.cache_len[b] = w.t0 + w.n > 0 ? (int32_t)group_of(w.t0 + w.n, s) : 0;
+          copy = w.n == 0;
         }
-        if (w.n == 0)
-          for (int k = lane; k < D; k += 32) a.tail_out[(int64_t)b * D + k] = a.tail_in[(int64_t)b * D + k];
+        for (uint32_t left = __ballot_sync(0xffffffffu, copy); left; left &= left - 1) {
+          const int64_t row = (int64_t)(b0 + __ffs(left) - 1) * D;
+          for (int k = lane; k < D; k += 32) a.tail_out[row + k] = a.tail_in[row + k];
+        }
       }
+    if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
   } else {
     // ======================= epilogue warps =======================
     const bool rope = ch >= R;                   // warp-uniform

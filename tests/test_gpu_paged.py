@@ -46,10 +46,11 @@ def test_append(dims, s, page_rows):
     ([1] * 40, list(range(40)), 2, {}),
     ([300, 45], [2, 9], 5, TINY),
     ([1200], [3], 1200, TINY),
-    ([1] * 300 + [0] * 40 + [3, 2], [i % 70 for i in range(342)], 2, dict(H=12)),
+    ([1] * 600 + [0] * 40 + [3, 2], [i % 70 for i in range(642)], 2, dict(H=12)),
     ([255, 0, 258], [129, 5, 0], 1, dict(H=16)),
-    ([2] * 150, [i % 9 for i in range(150)], 4, dict(H=5)),
-], ids=["ragged", "s3", "s32", "s64", "s300", "decode40", "tiny", "onegroup", "decode300", "s1", "pairs"])
+    ([2] * 270, [i % 9 for i in range(270)], 4, dict(H=5)),
+    ([250, 200], [3, 0], 2, {}),
+], ids=["ragged", "s3", "s32", "s64", "s300", "decode40", "tiny", "onegroup", "decode600", "s1", "pairs", "below"])
 def test_append_long(new, past, s, dims):
     b = Batch(new, past, s=s, page_rows=16, seed=77, **dims)
     b.check_append(b.append())
@@ -71,8 +72,8 @@ def test_append_options(dims):
     b = Batch(count=[4, 2, 0, -3], **kw)
     b.check_append(b.append())
     # the same with tokens enough for the long-chunk kernel
-    kw = dict(kw, new=[150, 9, 200, 2])
-    for make in (dict(pad=8), dict(count=[90, 20, 0, 1])):
+    kw = dict(kw, new=[310, 9, 200, 2])
+    for make in (dict(pad=8), dict(count=[190, 20, 0, 1])):
         b = Batch(spare_tokens=5, **make, **kw)
         b.check_append(b.append(q="count" in make))
     b = Batch(**kw)
@@ -146,7 +147,7 @@ def test_append_in_pieces_and_taken_back(dims):
         assert torch.equal(back.d_pages[at][: back.D], few.d_pages[at][: few.D])
 
 
-@pytest.mark.parametrize("more", [[], [1] * 300], ids=["few", "many"])
+@pytest.mark.parametrize("more", [[], [1] * 520], ids=["few", "many"])
 def test_append_refuses_on_the_device(more):
     """Sequences that do not fit take nothing and say why; the others are not disturbed."""
     new, past, s = [3, 3, 3, 3] + more, [4, 30, 2, 5] + [6] * len(more), 2
