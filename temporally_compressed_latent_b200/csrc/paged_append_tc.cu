@@ -103,15 +103,27 @@ __device__ __forceinline__ float gated(float v, float y) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return v * r;
 }
+// The same for two columns, y = (g + bc) p: sums and products two an instruction
+// (packed fp32).
+__device__ __forceinline__ void gated2(float& v0, float& v1, uint32_t g0, uint32_t g1, float bc, float p0, float p1) {
+  asm("{\n .reg .b64 g, b, p, v, o;\n .reg .f32 x, y;\n"
+      " mov.b64 g, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 p, {%5, %6};\n mov.b64 v, {%0, %1};\n"
+      " add.rn.f32x2 g, g, b;\n mul.rn.f32x2 g, g, p;\n"
+      " mov.b64 {x, y}, g;\n ex2.approx.ftz.f32 x, x;\n ex2.approx.ftz.f32 y, y;\n mov.b64 g, {x, y};\n"
+      " mov.b64 o, {0f3F800000, 0f3F800000};\n add.rn.f32x2 g, g, o;\n"
+      " mov.b64 {x, y}, g;\n rcp.approx.ftz.f32 x, x;\n rcp.approx.ftz.f32 y, y;\n mov.b64 g, {x, y};\n"
+      " mul.rn.f32x2 v, v, g;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(v0), "+f"(v1) : "f"(__uint_as_float(g0)), "f"(__uint_as_float(g1)), "f"(bc), "f"(p0), "f"(p1));
+}
 constexpr float kNegLog2e = -1.4426950408889634f;
 
-// Rotates the queries: a warp takes QROWS token rows, all their loads in flight
-// before the first angle; a half of the warp computes a token's 16 angles, a
-// lane turns 16 bytes of a row.  It reads nothing that the append kernel
-// writes, so it starts as soon as that one has started (by then everything
-// before both is complete) and waits for it only at its end, so that what
-// follows finds both done.
-constexpr int QROWS = 4, QT = 256;
+// Rotates the queries: a warp takes QROWS token rows (one search for their
+// sequences), four a step with the next step's loads in flight; a half of the
+// warp computes a token's 16 angles, a lane turns 16 bytes of a row.  It reads
+// nothing that the append kernel writes, so it starts as soon as that one has
+// started (by then everything before both is complete) and waits for it only
+// at its end, so that what follows finds both done.
+constexpr int QROWS = 8, QT = 256;
 __global__ void __launch_bounds__(QT, 4) paged_rotate_kernel(const __grid_constant__ PagedAppendArgs a) {
   const int lane = threadIdx.x & 31, words = a.H * (DR / 8);
   const int64_t i = ((int64_t)blockIdx.x * (QT / 32) + (threadIdx.x >> 5)) * QROWS;
@@ -119,35 +131,45 @@ __global__ void __launch_bounds__(QT, 4) paged_rotate_kernel(const __grid_consta
     const uint4* src = reinterpret_cast<const uint4*>(a.q_rope);
     uint4* dst = reinterpret_cast<uint4*>(a.q_rope_out);
     const uint64_t turn = a.rotate ? a.rope.turns[lane & 15] : 0;
-    int b[1];
-    warp_sequences<1>(a.c, i, b);
-    AppendWin w = seq_win(a.c, b[0] < 0 ? 0 : b[0]);
-    append_fit(a, w, false);
+    int b;
+    AppendWin w;
+    warp_windows(a, i, b, w);
     const int64_t place = i + lane - w.first;
     const uint32_t taken =
-        __ballot_sync(0xffffffffu, lane < QROWS && i + lane < a.c.N && b[0] >= 0 && place >= 0 && place < w.n);
+        __ballot_sync(0xffffffffu, lane < QROWS && i + lane < a.c.N && b >= 0 && place >= 0 && place < w.n);
     const uint32_t pos = (uint32_t)w.t0 + (uint32_t)place;
+#pragma unroll 1
     for (int word = lane; word < (words + 31) / 32 * 32; word += 32) {
-      uint4 v[QROWS];
+      uint4 v[4], next[4];
+      auto load = [&](uint4 (&x)[4], int k) {
 #pragma unroll
-      for (int k = 0; k < QROWS; ++k) {
-        v[k] = make_uint4(0, 0, 0, 0);
-        if ((taken >> k & 1) && word < words) v[k] = src[(i + k) * words + word];
-      }
+        for (int h = 0; h < 4; ++h) {
+          x[h] = make_uint4(0, 0, 0, 0);
+          if ((taken >> (k + h) & 1) && word < words) x[h] = src[(i + k + h) * words + word];
+        }
+      };
+      load(next, 0);
+#pragma unroll 1
+      for (int k = 0; k < QROWS; k += 4) {
 #pragma unroll
-      for (int k = 0; k < QROWS; k += 2) {
-        const float2 cs = rope_cos_sin(__shfl_sync(0xffffffffu, pos, k + (lane >> 4)), turn);
+        for (int h = 0; h < 4; ++h) v[h] = next[h];
+        if (k + 4 < QROWS) load(next, k + 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[4] = {v[k + h].x, v[k + h].y, v[k + h].z, v[k + h].w};
+        for (int g = 0; g < 4; g += 2) {
+          const float2 cs = rope_cos_sin(__shfl_sync(0xffffffffu, pos, k + g + (lane >> 4)), turn);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {          // pair 4 (word mod 4) + e
-            const int sl = 16 * h + 4 * (word & 3) + e;
-            const float co = __shfl_sync(0xffffffffu, cs.x, sl), si = __shfl_sync(0xffffffffu, cs.y, sl);
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
-            x[e] = pack_bf16x2(f.x * co - f.y * si, f.x * si + f.y * co);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[4] = {v[g + h].x, v[g + h].y, v[g + h].z, v[g + h].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {        // pair 4 (word mod 4) + e
+              const int sl = 16 * h + 4 * (word & 3) + e;
+              const float co = __shfl_sync(0xffffffffu, cs.x, sl), si = __shfl_sync(0xffffffffu, cs.y, sl);
+              const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+              x[e] = pack_bf16x2(f.x * co - f.y * si, f.x * si + f.y * co);
+            }
+            if ((taken >> (k + g + h) & 1) && word < words)
+              dst[(i + k + g + h) * words + word] = make_uint4(x[0], x[1], x[2], x[3]);
           }
-          if ((taken >> (k + h) & 1) && word < words) dst[(i + k + h) * words + word] = make_uint4(x[0], x[1], x[2], x[3]);
         }
       }
     }
@@ -510,7 +532,7 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = gated(v[k], (__uint_as_float(g[k]) + bc) * pc[k]);
+          for (int k = 0; k < 16; k += 2) gated2(v[k], v[k + 1], g[k], g[k + 1], bc, pc[k], pc[k + 1]);
           // the sums, in token order (what a column before the first open group
           // holds is never stored); a chunk that goes on in an open group starts
           // at its tail
