@@ -266,14 +266,14 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
 
 }  // namespace vfy
 
-cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
-  // As many blocks a sequence as leave all of them resident at once (a
-  // sequence's chain of latencies is then paid once): 96 sequences of 131072
-  // entries take XX us with 8 blocks each, YY with 6; at least as many as keep
-  // a block's notes in its shared memory.
-  int cl = sms * vfy::BLOCKS / a.B;
-  const int least = (a.V / vfy::RUN + 2) / vfy::MAXRUNS + 1;
-  cl = cl < least ? least : (cl > vfy::MAXCL ? vfy::MAXCL : cl);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st) {
+  // A block of the cluster per 4096 entries, up to 8 (which also keeps its notes
+  // within its shared memory): one sequence of 32000 entries takes 9.5 us with
+  // 2 blocks, 7.0 with 4, 6.1 with 8; 96 of 131072 take 35.7, 27.6 and 27.6 (more
+  // blocks than fit at once there, so that some stream while others wait for
+  // their first reads); with small vocabularies more blocks would only wait.
+  int cl = (a.V + 4095) / 4096;
+  cl = cl < vfy::MAXCL ? cl : vfy::MAXCL;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cl;
