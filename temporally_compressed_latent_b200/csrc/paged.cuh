@@ -219,6 +219,17 @@ struct Item {
   int slot;         // partial-result slot, or -1: the whole item is here, its results go out directly
 };
 
+// An upper bound of the blocks that get a share, from what the host knows (N
+// tokens of B sequences, tables of `rows` cache rows).  Where it is one, no item
+// is split and nothing is left to join.
+inline int most_blocks(const PlanArgs& a, int64_t N, int64_t B, int64_t rows, int grid) {
+  int64_t items = (N + a.tpt - 1) / a.tpt + B;
+  if (items > N) items = N;
+  const int64_t tiles = ((rows + 7) / 8 + (a.tpt + 7) / 8 + a.q - 1) / a.q, C = items * (a.item_cost + tiles);
+  if (C <= 2 * a.min_share) return 1;
+  const int64_t g = (C + a.min_share - 1) / a.min_share;
+  return g < grid ? (int)g : grid;
+}
 // Blocks that get a share: no more than give each min_share of the weight C.
 __device__ __forceinline__ int64_t share_blocks(const PlanArgs& a, int64_t C, int grid) {
   if (C >= (int64_t)a.min_share * grid) return grid;
@@ -287,7 +298,8 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
   __syncthreads();
   if (lane == 0) atomicMax(&sh->most, most);
   int64_t base = 0, C = 0;
-  for (int w = 0; w < NT / 32; ++w) {
+  const int warps = per == 1 ? (c.B + 31) / 32 : NT / 32;  // warps that have sequences
+  for (int w = 0; w < warps; ++w) {
     if (w < warp) base += sh->warp_sum[w];
     C += sh->warp_sum[w];
   }

@@ -233,14 +233,15 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   a.plan.item_cost = 2;
   a.plan.min_share = sh.tc ? 4 : 1;
   a.plan.div_s = fast_div((uint32_t)dims->s);
+  const int grid = most_blocks(a.plan, chunk->N, B, (int64_t)cache->table_pages * cache->page_rows, sh.grid);
   if (sh.tc) {
     PagedAttnMaps maps;
     if (!paged_maps(&maps, a)) return MTLA_ERR_CUDA;
-    if (launch_paged_attn_tc(a, maps, sh.grid, cs) != cudaSuccess) return MTLA_ERR_CUDA;
-  } else if (launch_paged_attn_simt(a, sh.grid, dims->dtype, cs) != cudaSuccess) {
+    if (launch_paged_attn_tc(a, maps, grid, cs) != cudaSuccess) return MTLA_ERR_CUDA;
+  } else if (launch_paged_attn_simt(a, grid, dims->dtype, cs) != cudaSuccess) {
     return MTLA_ERR_CUDA;
   }
-  return from_cuda(launch_paged_combine(a, sh.grid, dims->dtype, cs));
+  return grid > 1 ? from_cuda(launch_paged_combine(a, grid, dims->dtype, cs)) : MTLA_OK;
 }
 
 mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, int64_t ld_p, const float* q,
