@@ -194,10 +194,12 @@ __device__ __forceinline__ int rows_below(const PlanArgs& a, int64_t t) { return
 __device__ __forceinline__ int item_tiles(const PlanArgs& a, int64_t t, int k) {
   return (((rows_below(a, t) + 7) >> 3) + ((k + 7) >> 3) + a.q - 1) >> (a.q == 8 ? 3 : 2);
 }
-// weight of a sequence's first m items (chunk of n tokens after t0)
-__device__ inline int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int64_t m) {
-  if (m == 0) return 0;
-  if (n <= a.tpt) return a.item_cost + item_tiles(a, t0 + n, n);  // one item
+// weight of a sequence's first m items (chunk of n tokens after t0).  (Of a
+// sequence with several: out of line, a kernel's start over single tokens
+// should not have to fetch past this code.)
+static __device__ __noinline__ int64_t items_weight_many(int s, int tpt, int q, int item_cost, FastDiv div_s, int64_t t0, int n,
+                                                         int64_t m) {
+  const PlanArgs a = {s, tpt, q, item_cost, 0, div_s};
   const int64_t full = n / a.tpt, k = m < full ? m : full;
   int64_t w = m * a.item_cost;
   if (k == 1) w += item_tiles(a, t0 + a.tpt, a.tpt);
@@ -206,6 +208,34 @@ __device__ inline int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int
                    (uint64_t)(t0 + a.tpt + 7ll * a.s - 1 + 8ll * a.s * (((a.tpt + 7) >> 3) + a.q - 1)));
   if (m > full) w += item_tiles(a, t0 + n, n - (int)full * a.tpt);
   return w;
+}
+__device__ __forceinline__ int64_t items_weight(const PlanArgs& a, int64_t t0, int n, int64_t m) {
+  if (m == 0) return 0;
+  if (n <= a.tpt) return a.item_cost + item_tiles(a, t0 + n, n);  // one item
+  return items_weight_many(a.s, a.tpt, a.q, a.item_cost, a.div_s, t0, n, m);
+}
+// weight of all of a sequence's items
+__device__ __forceinline__ int64_t seq_weight(const PlanArgs& a, int64_t t0, int n) {
+  if (n <= a.tpt) return n > 0 ? a.item_cost + item_tiles(a, t0 + n, n) : 0;
+  return items_weight_many(a.s, a.tpt, a.q, a.item_cost, a.div_s, t0, n, (n + a.tpt - 1) / a.tpt);
+}
+// The item of a sequence with several that holds offset rem of its weight: the
+// largest whose earlier items weigh no more (32 candidates a round, by a warp).
+static __device__ __noinline__ int find_item(int s, int tpt, int q, int item_cost, FastDiv div_s, int64_t t0, int n, int64_t rem) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, up = (n + tpt - 1) / tpt;
+  while (up - lo > 1) {
+    const int step = (up - lo - 1 + 31) / 32, at = lo + 1 + lane * step;
+    const bool le = at < up && items_weight_many(s, tpt, q, item_cost, div_s, t0, n, at) <= rem;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    if (k == 0) {
+      up = lo + 1;
+    } else {
+      lo = lo + 1 + (k - 1) * step;
+      if (lo + step < up) up = lo + step;
+    }
+  }
+  return lo;
 }
 
 // One item's part in a block.
@@ -282,7 +312,7 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
   if (tid == 0) sh->most = 0;
   for (int b = b0; b < b1; ++b) {
     const SeqWin w = attn_win(c, p, a.div_s, b, x == 0 ? dev_err : nullptr);
-    sum += items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
+    sum += seq_weight(a, w.t0, w.n);
     most = most > w.n ? most : w.n;
     if (per == 1) win[b] = w;
   }
@@ -316,7 +346,7 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
       int b = b0;
       for (; b + 1 < b1; ++b) {  // (not taken where every thread has one)
         const SeqWin w = attn_win(c, p, a.div_s, b, nullptr);
-        const int64_t k = items_weight(a, w.t0, w.n, (w.n + a.tpt - 1) / a.tpt);
+        const int64_t k = seq_weight(a, w.t0, w.n);
         if (lo < at + k) break;
         at += k;
       }
@@ -365,24 +395,9 @@ struct ItemWalk {
     hi = share_lo(C, G, x + 1);
     b = sh->b;
     load(c, p, a, b);
-    // the item of sequence b at offset pos - before: the largest tile whose
-    // earlier tiles weigh no more (32 candidates a round)
     const int n = __shfl_sync(0xffffffffu, w_n, 0);
-    const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, 0), rem = pos - sh->before;
-    const int lane = threadIdx.x & 31;
-    int lo = 0, up = n <= a.tpt ? 1 : (n + a.tpt - 1) / a.tpt;
-    while (up - lo > 1) {
-      const int step = (up - lo - 1 + 31) / 32, at = lo + 1 + lane * step;
-      const bool le = at < up && items_weight(a, t0, n, at) <= rem;
-      const int k = __popc(__ballot_sync(0xffffffffu, le));
-      if (k == 0) {
-        up = lo + 1;
-      } else {
-        lo = lo + 1 + (k - 1) * step;
-        if (lo + step < up) up = lo + step;
-      }
-    }
-    tile = lo;
+    const int64_t t0 = __shfl_sync(0xffffffffu, w_t0, 0);
+    tile = n <= a.tpt ? 0 : find_item(a.s, a.tpt, a.q, a.item_cost, a.div_s, t0, n, pos - sh->before);
     start = sh->before + items_weight(a, t0, n, tile);
   }
 
