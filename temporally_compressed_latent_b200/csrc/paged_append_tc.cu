@@ -22,9 +22,11 @@
 //  * Two metadata warps work a tile ahead: they find the tokens' sequences and
 //    leave P rows, pool rows, positions and bit masks (which tokens open a
 //    group, end a chunk, ...) in shared memory, and send the tile's P rows
-//    towards L2.  The epilogue's 12 warps take 32 columns each in chunks of 16;
-//    they are bound by issue and by the latency of their chain, so P comes to
-//    shared memory by asynchronous copies while the tile before is stored, and
+//    towards L2.  The epilogue's 12 warps take 32 columns each in chunks of 8
+//    (2048 tokens of four prompts, 32 query rows a token, on B200: 32.3 us; of
+//    16 columns 33.0, whose longer code no longer stays in the instruction
+//    cache; of 4 35.2).  They are bound by issue and by the latency of their
+//    chain, so P comes to shared memory by asynchronous copies while the tile before is stored, and
 //    finished rows leave through a staging block, 16 bytes of eight rows a step.
 //  * RoPE: an exact angle every 8 tokens of a run of positions and a rotation
 //    by the pair's own angle between them (at most seven single-precision
@@ -46,6 +48,7 @@ constexpr int KS = 2 * KB;                     // stages: two tiles
 constexpr int KRBLK = NTOK * DR * 2;           // RoPE keys of a tile: 8192 B
 constexpr int NWARPS = 16, NT = 32 * NWARPS;
 constexpr int NPART = NWARPS / 4, PCOL = NTOK / NPART;  // column parts of a tile (4) and their columns (32)
+constexpr int CH = 8;                          // columns of a chunk
 constexpr int NEPI = 3 * NPART;                // epilogue warps
 constexpr int TMA_WARP = 3, MMA_WARP = 7, META_WARP0 = 11, META_WARP1 = 15;  // warps of the padding quarter
 constexpr uint32_t TMEM_COLS = 512, ACC_STRIDE = 128, HI_COL = 256, LO_COL = 384;
@@ -82,13 +85,10 @@ static_assert(OFF_ROPE % 8 == 0 && sizeof(Meta) % 16 == 0 && OFF_META % 16 == 0 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr) : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -457,10 +457,10 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
         const uint32_t vrow = rope ? smem_u32(sm + OFF_KR + ab * KRBLK) + (uint32_t)(lane >> 1) * 4 : sB + (sb + c_kb) * BBLK + c_in;
         // Columns before cb belong to a group that began before them: it is
         // summed again from its start in the chunk.  A few of them singly (same
-        // P, and the tail if that start is the chunk's), more in chunks of 16.
+        // P, and the tail if that start is the chunk's), more in chunks of 8.
         const int back = mt.back[cb], c1 = cb - back;
         const bool single = back > 0 && back < 8 && cb == p0;
-        const int c_beg = single ? p0 : c1 & ~15;
+        const int c_beg = single ? p0 : c1 & ~(CH - 1);
         float ph = 0.f, run = 0.f;
         if (single) {
           ph = __ldg(Pc + (int64_t)mt.prow[cb] * D);
@@ -491,40 +491,40 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
-        for (int c0 = c_beg; c0 < ce; c0 += 16) {
-          uint32_t g[16];
-          tmem_ld16(acc + c0, g);
+        for (int c0 = c_beg; c0 < ce; c0 += CH) {
+          uint32_t g[CH];
+          tmem_ld8(acc + c0, g);
           const int word = c0 >> 5, bit = c0 & 31;
-          float v[16], pc[16];
+          float v[CH], pc[CH];
           if (c0 >= p0) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(pc[k]) : "r"(pbuf + (c0 - p0 + k) * 128));
+            for (int k = 0; k < CH; ++k) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(pc[k]) : "r"(pbuf + (c0 - p0 + k) * 128));
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) pc[k] = __ldg(Pc + (int64_t)mt.prow[c0 + k] * D);
+            for (int k = 0; k < CH; ++k) pc[k] = __ldg(Pc + (int64_t)mt.prow[c0 + k] * D);
           }
           if (rope) {
             const uint32_t at = vrow + (uint32_t)c0 * (DR * 2);
-            uint32_t pair[16];
+            uint32_t pair[CH];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[k]) : "r"(at + k * (DR * 2)));
-            if ((mt.turn[word] >> bit & 0xfffeu) == 0) {  // one run of positions
+            for (int k = 0; k < CH; ++k) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(pair[k]) : "r"(at + k * (DR * 2)));
+            if ((mt.turn[word] >> bit & 0xfeu) == 0) {  // one run of positions
               const uint32_t first = mt.pos[c0];
               float2 cs = make_float2(1.f, 0.f);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
+              for (int k = 0; k < CH; ++k) {
                 cs = (k & 7) == 0 ? rope_cos_sin(first + k, turn)
                                   : make_float2(cs.x * step.x - cs.y * step.y, cs.x * step.y + cs.y * step.x);
                 v[k] = turned(pair[k], cs);
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = turned(pair[k], rope_cos_sin(mt.pos[c0 + k], turn));
+              for (int k = 0; k < CH; ++k) v[k] = turned(pair[k], rope_cos_sin(mt.pos[c0 + k], turn));
             }
           } else {
             const uint32_t at = vrow + (uint32_t)(c0 >> 3) * 1024;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < CH; ++k) {
               uint16_t raw;
               asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(at + (k >> 3) * 1024 + (k & 7) * 128 + xo[k & 7]));
               v[k] = __bfloat162float(__ushort_as_bfloat16(raw));
@@ -532,31 +532,31 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) gated2(v[k], v[k + 1], g[k], g[k + 1], bc, pc[k], pc[k + 1]);
+          for (int k = 0; k < CH; k += 2) gated2(v[k], v[k + 1], g[k], g[k + 1], bc, pc[k], pc[k + 1]);
           // the sums, in token order (what a column before the first open group
           // holds is never stored); a chunk that goes on in an open group starts
           // at its tail
-          const uint32_t open = mt.open[word] >> bit, carry = mt.carry[word] >> bit & 0xffffu;
+          const uint32_t open = mt.open[word] >> bit, carry = mt.carry[word] >> bit & 0xffu;
           if (carry) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < CH; ++k)
               if (carry >> k & 1) v[k] += a.tail_in[(int64_t)mt.seq[c0 + k] * D + ch];
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < CH; ++k) {
             run = (open >> k & 1 ? 0.f : run) + v[k];
             v[k] = run;
           }
           if (c0 >= p0) {
-            const uint32_t last = mt.last[word] >> bit & 0xffffu;
+            const uint32_t last = mt.last[word] >> bit & 0xffu;
             if (last) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
+              for (int k = 0; k < CH; ++k)
                 if ((last >> k & 1) && c0 + k >= cb && c0 + k < ce) a.tail_out[(int64_t)mt.seq[c0 + k] * D + ch] = v[k];
             }
             const uint32_t at = ost_ch + (uint32_t)(c0 - p0) * 64;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
+            for (int k = 0; k < CH; k += 2) {
               const uint32_t w = pack_bf16x2(v[k], v[k + 1]);
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + k * 64), "h"((uint16_t)(w & 0xffffu)) : "memory");
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + k * 64 + 64), "h"((uint16_t)(w >> 16)) : "memory");
