@@ -605,6 +605,6 @@ struct VerifyArgs {
   int32_t *n_keep, *next_token;
   int32_t* dev_err;
 };
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st);
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st);
 
 }  // namespace mtla

@@ -271,7 +271,9 @@ mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, 
   a.n_keep = n_keep;
   a.next_token = next_token;
   a.dev_err = dev_err;
-  return from_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));
+  const int sms = current_device_sms();
+  if (sms <= 0) return MTLA_ERR_CUDA;
+  return from_cuda(launch_verify(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

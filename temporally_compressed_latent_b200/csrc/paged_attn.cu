@@ -314,13 +314,14 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
 // ----------------------------------------------------------------------------
 // Combine: block (g, y) finishes rows of the split item that ends in block g of
 // the attention grid: out = sum_x 2^(m_x - M) O_x / sum_x 2^(m_x - M) l_x over
-// its parts.  Four channels a thread, 64 threads a row, two rows at once when
-// parts are few, and one row with the parts split in two when they are many (a
-// long cache under one token: the loads' latency bounds it, four parts in
-// flight).  At 64 registers a thread a block fits beside the attention's and
+// its parts.  A warp takes a row, eight channels a lane and three parts in flight
+// (the loads' latency bounds a decode step's few rows, the instructions a long
+// chunk's many: with 64 threads a row the latter took half as long again); where
+// parts are many (a long cache under one token) the block's four warps share a
+// row's parts.  At 64 registers a thread a block fits beside the attention's and
 // waits there for its end.
 // ----------------------------------------------------------------------------
-constexpr int CNT = 128;
+constexpr int CNT = 128, CNW = CNT / 32, CNP = 3;
 
 template <typename T>
 __global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
@@ -329,87 +330,105 @@ __global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_cons
   const SplitDesc* const d = a.part.desc + blockIdx.x;
   const int live = d->ntok * a.H;
   if (live == 0) return;
-  __shared__ float red[64][6];
+  __shared__ float4 red[CNW][2][32];
+  __shared__ float2 red_ml[CNW];
   const int first = d->first, parts = (int)blockIdx.x - first + 1;  // every block between has one (their shares are not empty)
   const int64_t row0 = (int64_t)d->row0 * a.H;
   const bool many = parts > 8;
-  const int sub = threadIdx.x >> 6, q0 = threadIdx.x & 63;
-  const int k_beg = many ? sub : 0, k_step = many ? 2 : 1, rows_at_once = many ? 1 : 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k_beg = many ? warp : 0, k_step = many ? CNW : 1, rows_at_once = many ? 1 : CNW;
   for (int r0 = blockIdx.y * rows_at_once; r0 < live; r0 += gridDim.y * rows_at_once) {
-    const int row = r0 + (many ? 0 : sub);
-    for (int e = 4 * q0; e < (a.r + 255) / 256 * 256; e += 256) {
-      const bool on = row < live && e < a.r;
+    const int row = r0 + (many ? 0 : warp);
+    if (row >= live) break;  // (never where the block has barriers: there row is block-uniform)
+    for (int e0 = 0; e0 < a.r; e0 += 256) {
+      const int e = e0 + 4 * lane;  // and e + 128
+      const bool on0 = e < a.r, on1 = e + 128 < a.r;
       float M = -INFINITY, L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (on) {
-        for (int k0 = k_beg; k0 < parts; k0 += 4 * k_step) {
-          float2 ml[4];
-          float4 o[4];
-          float Mn = M;
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int k0 = k_beg; k0 < parts; k0 += CNP * k_step) {
+        float2 ml[CNP];
+        float4 o[CNP][2];
+        float Mn = M;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int k = k0 + u * k_step;
-            ml[u] = make_float2(-INFINITY, 0.f);
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < parts) {
-              const int64_t prow = (int64_t)(2 * (first + k) + (k == 0 ? 1 : 0)) * a.rows + row;
-              ml[u] = a.part.ml[prow];
-              o[u] = *reinterpret_cast<const float4*>(a.part.o + prow * a.r + e);
-            }
+        for (int u = 0; u < CNP; ++u) {
+          const int k = k0 + u * k_step;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          o[u][0] = o[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < parts) {
+            const int64_t prow = (int64_t)(2 * (first + k) + (k == 0 ? 1 : 0)) * a.rows + row;
+            ml[u] = a.part.ml[prow];
+            const float* const src = a.part.o + prow * a.r + e;
+            if (on0) o[u][0] = *reinterpret_cast<const float4*>(src);
+            if (on1) o[u][1] = *reinterpret_cast<const float4*>(src + 128);
           }
+        }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, ml[u].x);
-          const float ref = Mn == -INFINITY ? 0.f : Mn, f = exp2f(M - ref);
-          M = Mn;
-          L *= f;
-          acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+        for (int u = 0; u < CNP; ++u) Mn = fmaxf(Mn, ml[u].x);
+        const float ref = Mn == -INFINITY ? 0.f : Mn, f = exp2f(M - ref);
+        M = Mn;
+        L *= f;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            // (a part with nothing visible to this row holds no values of it)
-            const float g = exp2f(ml[u].x - ref);
-            if (g > 0.f) {
-              L = fmaf(ml[u].y, g, L);
-              acc.x = fmaf(o[u].x, g, acc.x);
-              acc.y = fmaf(o[u].y, g, acc.y);
-              acc.z = fmaf(o[u].z, g, acc.z);
-              acc.w = fmaf(o[u].w, g, acc.w);
-            }
+        for (int h = 0; h < 2; ++h) {
+          acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+        }
+#pragma unroll
+        for (int u = 0; u < CNP; ++u) {
+          // (a part with nothing visible to this row holds no values of it)
+          const float g = exp2f(ml[u].x - ref);
+          if (!(g > 0.f)) continue;
+          L = fmaf(ml[u].y, g, L);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            acc[h].x = fmaf(o[u][h].x, g, acc[h].x);
+            acc[h].y = fmaf(o[u][h].y, g, acc[h].y);
+            acc[h].z = fmaf(o[u][h].z, g, acc[h].z);
+            acc[h].w = fmaf(o[u][h].w, g, acc[h].w);
           }
         }
       }
-      if (many) {  // join the two halves of the parts (block-uniform branch)
+      if (many) {  // join the four warps' shares of the parts (block-uniform branch)
         __syncthreads();
-        if (sub == 1) {
-          red[q0][0] = acc.x;
-          red[q0][1] = acc.y;
-          red[q0][2] = acc.z;
-          red[q0][3] = acc.w;
-          red[q0][4] = M;
-          red[q0][5] = L;
+        red[warp][0][lane] = acc[0];
+        red[warp][1][lane] = acc[1];
+        if (lane == 0) red_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (warp != 0) continue;
+        float Mt = M;
+#pragma unroll
+        for (int w = 1; w < CNW; ++w) Mt = fmaxf(Mt, red_ml[w].x);
+        const float ref = Mt == -INFINITY ? 0.f : Mt, f = exp2f(M - ref);
+        M = Mt;
+        L *= f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
         }
-        __syncthreads();
-        if (sub == 0) {
-          const float M1 = red[q0][4], Mt = fmaxf(M, M1), ref = Mt == -INFINITY ? 0.f : Mt;
-          const float f0 = exp2f(M - ref), f1 = exp2f(M1 - ref);
-          L = L * f0 + red[q0][5] * f1;
-          acc.x = acc.x * f0 + red[q0][0] * f1;
-          acc.y = acc.y * f0 + red[q0][1] * f1;
-          acc.z = acc.z * f0 + red[q0][2] * f1;
-          acc.w = acc.w * f0 + red[q0][3] * f1;
-          M = Mt;
+#pragma unroll
+        for (int w = 1; w < CNW; ++w) {
+          const float g = exp2f(red_ml[w].x - ref);
+          L = fmaf(red_ml[w].y, g, L);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 o = red[w][h][lane];
+            acc[h].x = fmaf(o.x, g, acc[h].x);
+            acc[h].y = fmaf(o.y, g, acc[h].y);
+            acc[h].z = fmaf(o.z, g, acc[h].z);
+            acc[h].w = fmaf(o.w, g, acc[h].w);
+          }
         }
       }
-      if (on && (!many || sub == 0)) {
-        const float inv = 1.f / L;
-        const int64_t orow = row0 + row;
-        if (a.lse && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
-        const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (a.out_f32 || sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + orow * a.r + e) = v;
-        } else {
-          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * a.r + e) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        }
+      const float inv = 1.f / L;
+      const int64_t orow = row0 + row;
+      if (a.lse && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 0 ? !on0 : !on1) continue;
+        const int64_t at = orow * a.r + e + 128 * h;
+        const float4 v = make_float4(acc[h].x * inv, acc[h].y * inv, acc[h].z * inv, acc[h].w * inv);
+        if (a.out_f32 || sizeof(T) == 4)
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = v;
+        else
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
     }
   }
@@ -470,10 +489,10 @@ cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cu
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // two rows at once a block, about four times (the rows of an item: the tokens
-  // of an average sequence, all heads)
+  // a row a warp, of a long chunk two to four (the rows of an item: the tokens of
+  // an average sequence, all heads)
   const int64_t item = (a.c.N + (int64_t)a.c.B - 1) / a.c.B * a.H, rows = item < a.rows ? item : a.rows;
-  const int64_t y = rows <= 32 ? (rows + 1) / 2 : 16;
+  const int64_t y = rows <= 8 ? rows : (rows <= 64 ? (rows + psimt::CNW - 1) / psimt::CNW : 16);
   cfg.gridDim = dim3((unsigned)grid, (unsigned)y);
   cfg.blockDim = dim3(psimt::CNT);
   cfg.stream = st;

@@ -30,9 +30,9 @@ namespace vfy {
 
 namespace cg = cooperative_groups;
 constexpr int MAXCL = 8;
-constexpr int NT = 256, NW = NT / 32, BLOCKS = 4;   // threads; resident blocks an SM
+constexpr int NT = 256, NW = NT / 32, BLOCKS = 3;   // threads; resident blocks an SM (of 4, 64 registers spill: 96 x 131072 2.5 us longer)
 constexpr int RUN = 256;                            // entries a warp sums at a time
-constexpr int MAXRUNS = 2304;                       // runs of a block (2^22 entries over 8 blocks: 2049)
+constexpr int MAXRUNS = 4104;                       // runs of a block (2^22 entries over 4 blocks: 4097)
 
 // entries that are NaN, infinite or not above zero count as zero
 __device__ __forceinline__ float clean(float x) { return x > 0.f && x <= 3.4028234663852886e38f ? x : 0.f; }
@@ -57,41 +57,57 @@ struct Weights {
   const float *p, *q;   // q: null where p alone counts
   int V, hole;          // hole: an entry without weight, or -1
   int shift;            // entries between that boundary and the row of p
-  bool qvec;            // q's row has the same shift
+  bool qvec;            // q is absent or its row has the same shift
   // eight positions of a run starting at j0: lane l's are j0 + 4 l .. + 3 and
-  // j0 + 128 + 4 l .. + 3
+  // j0 + 128 + 4 l .. + 3; those outside the row, and all of an absent q, are zero
   __device__ __forceinline__ void load(int j0, float (&a)[8], float (&b)[8]) const {
-    const int lane = threadIdx.x & 31;
+    const int v0 = j0 + 4 * (threadIdx.x & 31) - shift;
+    if (j0 >= shift && j0 + RUN - shift <= V && qvec) {  // (warp-uniform) the whole run, in quadruples
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int v = j0 + 128 * h + 4 * lane - shift;
-      const bool whole = v >= 0 && v + 4 <= V;
-      if (whole) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p + v));
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p + v0 + 128 * h));
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q) y = __ldg(reinterpret_cast<const float4*>(q + v0 + 128 * h));
         a[4 * h] = x.x; a[4 * h + 1] = x.y; a[4 * h + 2] = x.z; a[4 * h + 3] = x.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[4 * h + e] = v + e >= 0 && v + e < V ? __ldg(p + v + e) : 0.f;
-      }
-      if (!q) continue;
-      if (whole && qvec) {
-        const float4 y = __ldg(reinterpret_cast<const float4*>(q + v));
         b[4 * h] = y.x; b[4 * h + 1] = y.y; b[4 * h + 2] = y.z; b[4 * h + 3] = y.w;
-      } else {
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[4 * h + e] = v + e >= 0 && v + e < V ? __ldg(q + v + e) : 0.f;
+      for (int k = 0; k < 8; ++k) {
+        const int v = v0 + 128 * (k >> 2) + (k & 3);
+        const bool in = v >= 0 && v < V;
+        a[k] = in ? __ldg(p + v) : 0.f;
+        b[k] = in && q ? __ldg(q + v) : 0.f;
       }
     }
   }
-  __device__ __forceinline__ void weigh(int j0, const float (&a)[8], const float (&b)[8], double (&w)[8]) const {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ void weigh(int j0, float (&a)[8], float (&b)[8], double (&w)[8]) const {
+    // one comparison for all of a lane's entries: as unsigned, the bits of those
+    // that do not count are the largest
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = clean(a[k]), y = q ? clean(b[k]) : 0.f;
-      // (a float difference has the sign of the exact one)
-      w[k] = x > y ? (double)x - (double)y : 0.0;
-      if (j0 + 128 * (k >> 2) + 4 * lane + (k & 3) - shift == hole) w[k] = 0.0;
+    for (int k = 0; k < 8; ++k) top = max(max(top, __float_as_uint(a[k])), __float_as_uint(b[k]));
+    if (top >= 0x7f800000u) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a[k] = clean(a[k]);
+        b[k] = clean(b[k]);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = (double)fmaxf(a[k], b[k]) - (double)b[k];
+    const int at = hole + shift - j0;  // the hole's position in this run
+    if (hole >= 0 && at >= 0 && at < RUN) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (128 * (k >> 2) + 4 * (int)(threadIdx.x & 31) + (k & 3) == at) w[k] = 0.0;
+    }
+  }
+  // the sum of a run's weights, to every lane
+  __device__ __forceinline__ double sum(int j0, float (&a)[8], float (&b)[8]) const {
+    double x[8];
+    weigh(j0, a, b, x);
+    return warp_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
   }
 };
 
@@ -145,7 +161,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
   w.q = a.q && dropped ? a.q + (int64_t)(first + drop) * a.ld_q : nullptr;
   w.V = a.V;
   w.shift = (int)(reinterpret_cast<uintptr_t>(w.p) >> 2 & 3);
-  w.qvec = w.q && (int)(reinterpret_cast<uintptr_t>(w.q) >> 2 & 3) == w.shift;
+  w.qvec = !w.q || (int)(reinterpret_cast<uintptr_t>(w.q) >> 2 & 3) == w.shift;
   // certain drafts (no q): the residual is p without the dropped token
   w.hole = !a.q && dropped ? a.tokens[first + drop + 1] : -1;
 
@@ -159,18 +175,17 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
     // the next run's loads are in flight while one is summed
     float pa[8], qa[8], pb[8], qb[8];
     if (warp < mine) w.load((r_beg + warp) * RUN, pa, qa);
-    for (int r = warp; r < mine; r += NW) {
-      if (r + NW < mine) w.load((r_beg + r + NW) * RUN, pb, qb);
-      double x[8];
-      w.weigh((r_beg + r) * RUN, pa, qa, x);
-      const double s = warp_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+    for (int r = warp; r < mine; r += 2 * NW) {
+      const bool more = r + NW < mine;
+      if (more) w.load((r_beg + r + NW) * RUN, pb, qb);
+      double s = w.sum((r_beg + r) * RUN, pa, qa);
       if (lane == 0) run_sum[r] = s;
       sum += s;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        pa[k] = pb[k];
-        qa[k] = qb[k];
-      }
+      if (!more) break;
+      if (r + 2 * NW < mine) w.load((r_beg + r + 2 * NW) * RUN, pa, qa);
+      s = w.sum((r_beg + r + NW) * RUN, pb, qb);
+      if (lane == 0) run_sum[r + NW] = s;
+      sum += s;
     }
     if (lane == 0) warp_total[warp] = sum;
     if (round == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -186,6 +201,7 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
     for (int r = 0; r < CL; ++r) total += totals[round & 1][r];
     if (total > 0.0 || !dropped || round > 0) break;
     w.q = nullptr;  // nothing above q: draw from p
+    w.qvec = true;
     w.hole = -1;
   }
   if (rank == 0 && tid == 0) a.n_keep[b] = drop + 1;
@@ -266,14 +282,16 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
 
 }  // namespace vfy
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t st) {
-  // A block of the cluster per 4096 entries, up to 8 (which also keeps its notes
-  // within its shared memory): one sequence of 32000 entries takes 9.5 us with
-  // 2 blocks, 7.0 with 4, 6.1 with 8; 96 of 131072 take 35.7, 27.6 and 27.6 (more
-  // blocks than fit at once there, so that some stream while others wait for
-  // their first reads); with small vocabularies more blocks would only wait.
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
+  // A block of the cluster per 4096 entries, up to 8, or up to 4 where 8 a
+  // sequence would not all be resident: one sequence of 32000 entries takes 6.2 us
+  // with 4 blocks and 5.5 with 8; 96 of 131072 take 21.2 with 4 (23.2 with 3) and
+  // 25.0 with 8, whose last clusters start when the first are through.  With small
+  // vocabularies more blocks would only wait.  (4 or 8 also keep a block's notes
+  // within its shared memory.)
+  const int most = (int64_t)a.B * vfy::MAXCL > (int64_t)vfy::BLOCKS * sms ? vfy::MAXCL / 2 : vfy::MAXCL;
   int cl = (a.V + 4095) / 4096;
-  cl = cl < vfy::MAXCL ? cl : vfy::MAXCL;
+  cl = cl < most ? cl : most;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cl;
