@@ -196,16 +196,23 @@ __device__ __forceinline__ int item_tiles(const PlanArgs& a, int64_t t, int k) {
 }
 // weight of a sequence's first m items (chunk of n tokens after t0).  (Of a
 // sequence with several: out of line, a kernel's start over single tokens
-// should not have to fetch past this code.)
+// should not have to fetch past this code.)  A few are added one by one; the
+// closed form's 64-bit divisions take as long as some dozens.
+constexpr int ADD_ITEMS = 32;
 static __device__ __noinline__ int64_t items_weight_many(int s, int tpt, int q, int item_cost, FastDiv div_s, int64_t t0, int n,
                                                          int64_t m) {
   const PlanArgs a = {s, tpt, q, item_cost, 0, div_s};
-  const int64_t full = n / a.tpt, k = m < full ? m : full;
   int64_t w = m * a.item_cost;
-  if (k == 1) w += item_tiles(a, t0 + a.tpt, a.tpt);
-  else if (k > 1)
-    w += floor_sum((uint64_t)k, 8ull * a.q * a.s, (uint64_t)a.tpt,
-                   (uint64_t)(t0 + a.tpt + 7ll * a.s - 1 + 8ll * a.s * (((a.tpt + 7) >> 3) + a.q - 1)));
+  if (m <= ADD_ITEMS) {
+    for (int i = 0; i < (int)m; ++i) {
+      const int e = (i + 1) * a.tpt < n ? (i + 1) * a.tpt : n;  // tokens up to the item's end
+      w += item_tiles(a, t0 + e, e - i * a.tpt);
+    }
+    return w;
+  }
+  const int64_t full = n / a.tpt, k = m < full ? m : full;
+  w += floor_sum((uint64_t)k, 8ull * a.q * a.s, (uint64_t)a.tpt,
+                 (uint64_t)(t0 + a.tpt + 7ll * a.s - 1 + 8ll * a.s * (((a.tpt + 7) >> 3) + a.q - 1)));
   if (m > full) w += item_tiles(a, t0 + n, n - (int)full * a.tpt);
   return w;
 }
@@ -508,7 +515,7 @@ constexpr int PSM = 32;  // M tile rows
 constexpr int PSN = 32;  // key tile rows
 int paged_simt_grid(int r, int d_R, int dtype, int sms);  // blocks of its persistent grid (0 on error)
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
-cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int sms, int dtype, cudaStream_t st);
 
 // tensor-core kernel (paged_attn_tc.cu): bf16, r = 256, d_R = 32
 constexpr int PTC_ROWS = 128;  // M tile rows

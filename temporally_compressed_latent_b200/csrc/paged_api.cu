@@ -241,7 +241,7 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   } else if (launch_paged_attn_simt(a, grid, dims->dtype, cs) != cudaSuccess) {
     return MTLA_ERR_CUDA;
   }
-  return grid > 1 ? from_cuda(launch_paged_combine(a, grid, dims->dtype, cs)) : MTLA_OK;
+  return grid > 1 ? from_cuda(launch_paged_combine(a, grid, current_device_sms(), dims->dtype, cs)) : MTLA_OK;
 }
 
 mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, int64_t ld_p, const float* q,

@@ -122,17 +122,6 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
     const Item it = *sit;
     const int live = it.ntok * a.H;
     const int64_t R8 = (it.R + 7) / 8 * 8;
-    // queries (rows past the live ones: zeros)
-    for (int k = tid; k < PSM * (D / 4); k += NT) {
-      const int i = k / (D / 4), e = (k - i * (D / 4)) * 4;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (i < live) {
-        const int64_t row = (int64_t)it.row0 * a.H + i;
-        if (e < a.r) ld4(reinterpret_cast<const T*>(a.q_abs) + row * a.r + e, v);
-        else ld4(reinterpret_cast<const T*>(a.q_rope) + row * a.d_R + (e - a.r), v);
-      }
-      *reinterpret_cast<float4*>(Qs + i * DP + e) = make_float4(v[0], v[1], v[2], v[3]);
-    }
     if (tid < PSM) {
       sm_m[tid] = -INFINITY;
       sm_l[tid] = 0.f;
@@ -171,7 +160,37 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // queries (rows past the live ones: zeros), eight threads a row; read while
+    // the first tile's rows are looked up
+    const int qi = tid >> 3;
+    const bool q_live = qi < live;
+    const int64_t q_row = (int64_t)it.row0 * a.H + qi;
+    auto q_quad = [&](int e) {
+      if (!q_live || e >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
+      return e < a.r ? ld4v(reinterpret_cast<const T*>(a.q_abs) + q_row * a.r + e)
+                     : ld4v(reinterpret_cast<const T*>(a.q_rope) + q_row * a.d_R + (e - a.r));
+    };
+    float4 qv[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) qv[k] = q_quad(4 * (tid & 7) + 32 * k);
     copy(look(it.kt0), 0);
+    for (int e0 = 4 * (tid & 7); e0 < D; e0 += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (e0 + 32 * k < D) *reinterpret_cast<float4*>(Qs + qi * DP + e0 + 32 * k) = qv[k];
+        if (e0 + 128 < D) qv[k] = q_quad(e0 + 128 + 32 * k);
+      }
+    }
+    // scores: this thread's rows r0, r0 + 16 (token, cache rows below it, virtual
+    // row of its own state; a row past the live ones sees nothing)
+    const int r0 = tid >> 4, c0 = tid & 15;
+    int64_t seen[2], own[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int tok = (r0 + 16 * k) / a.H;
+      seen[k] = tok < it.ntok ? rows_below(a.plan, it.t + tok) : 0;
+      own[k] = tok < it.ntok ? R8 + tok : -1;
+    }
     int64_t ahead = it.kt0 + 1 < it.kt1 ? look(it.kt0 + 1) : -1;
 
     for (int kt = it.kt0; kt < it.kt1; ++kt) {
@@ -186,7 +205,6 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       }
       __syncthreads();
       // scores: rows r0, r0 + 16; keys c0, c0 + 16
-      const int r0 = tid >> 4, c0 = tid & 15;
       uint64_t t00 = 0, t01 = 0, t10 = 0, t11 = 0;
 #pragma unroll 2
       for (int e = 0; e < D; e += 4) {
@@ -201,16 +219,14 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       }
       auto both = [](uint64_t v) { const float2 f = unpack2(v); return f.x + f.y; };
       const float s00 = both(t00), s01 = both(t01), s10 = both(t10), s11 = both(t11);
-      auto put = [&](int i, int c, float v) {
-        const int tok = i / a.H;
-        const int64_t g = v0 + c, seen = rows_below(a.plan, it.t + tok);
-        const bool vis = g < seen || g == R8 + tok;
-        Ss[c * (PSM + 4) + i] = vis && tok < it.ntok ? v * a.scale_log2 : -INFINITY;
+      auto put = [&](int k, int c, float v) {
+        const int64_t g = v0 + c;
+        Ss[c * (PSM + 4) + r0 + 16 * k] = g < seen[k] || g == own[k] ? v * a.scale_log2 : -INFINITY;
       };
-      put(r0, c0, s00);
-      put(r0, c0 + 16, s01);
-      put(r0 + 16, c0, s10);
-      put(r0 + 16, c0 + 16, s11);
+      put(0, c0, s00);
+      put(0, c0 + 16, s01);
+      put(1, c0, s10);
+      put(1, c0 + 16, s11);
       __syncthreads();
       {  // softmax: eight lanes a row, four keys each
         const int i = tid >> 3, k0 = tid & 7;
@@ -312,46 +328,79 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
 }
 
 // ----------------------------------------------------------------------------
-// Combine: block (g, y) finishes rows of the split item that ends in block g of
-// the attention grid: out = sum_x 2^(m_x - M) O_x / sum_x 2^(m_x - M) l_x over
-// its parts.  A warp takes a row, eight channels a lane and three parts in flight
-// (the loads' latency bounds a decode step's few rows, the instructions a long
-// chunk's many: with 64 threads a row the latter took half as long again); where
-// parts are many (a long cache under one token) the block's four warps share a
-// row's parts.  At 64 registers a thread a block fits beside the attention's and
-// waits there for its end.
+// Combine: block (x, y) finishes rows of the split item that ends in block x of
+// the attention grid, or of the x-th one (`nth`, see launch_paged_combine):
+//   out = sum_x 2^(m_x - M) O_x / sum_x 2^(m_x - M) l_x
+// over its parts x.  A row takes a warp, eight channels a lane and three parts
+// in flight (the loads' latency bounds a decode step's few rows, the
+// instructions a long chunk's many: with 64 threads a row the latter took half
+// as long again), or two or four warps, which share its parts, where there are
+// more parts than that and blocks enough for all rows at once.  At 64 registers a thread a block fits beside the attention's and waits there for its
+// end.
 // ----------------------------------------------------------------------------
 constexpr int CNT = 128, CNW = CNT / 32, CNP = 3;
 
 template <typename T>
-__global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a, int nth) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const SplitDesc* const d = a.part.desc + blockIdx.x;
-  const int live = d->ntok * a.H;
-  if (live == 0) return;
   __shared__ float4 red[CNW][2][32];
   __shared__ float2 red_ml[CNW];
-  const int first = d->first, parts = (int)blockIdx.x - first + 1;  // every block between has one (their shares are not empty)
-  const int64_t row0 = (int64_t)d->row0 * a.H;
-  const bool many = parts > 8;
+  __shared__ uint32_t ends[4 * CNW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k_beg = many ? warp : 0, k_step = many ? CNW : 1, rows_at_once = many ? 1 : CNW;
+  int g = blockIdx.x;
+  if (nth > 0) {  // the x-th of the nth notes that is not empty
+    int left = blockIdx.x;
+    g = -1;
+    for (int g0 = 0; g0 < nth && g < 0; g0 += 4 * CNT) {
+      bool some[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = g0 + k * CNT + (int)threadIdx.x;
+        some[k] = at < nth && a.part.desc[at].ntok > 0;
+      }
+      if (g0 > 0) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t m = __ballot_sync(0xffffffffu, some[k]);
+        if (lane == 0) ends[k * CNW + warp] = m;
+      }
+      __syncthreads();
+      for (int w = 0; w < 4 * CNW; ++w) {
+        uint32_t m = ends[w];
+        const int c = __popc(m);
+        if (left < c) {
+          for (; left > 0; --left) m &= m - 1;
+          g = g0 + 32 * w + __ffs(m) - 1;
+          break;
+        }
+        left -= c;
+      }
+    }
+    if (g < 0) return;
+  }
+  const SplitDesc* const d = a.part.desc + g;
+  const int live = d->ntok * a.H;
+  if (live == 0) return;
+  const int first = d->first, parts = g - first + 1;  // every block between has one (their shares are not empty)
+  const int64_t row0 = (int64_t)d->row0 * a.H;
+  int W = 1;  // warps a row
+  while (W < CNW && W * CNP < parts && live * 2 * W <= CNW * (int)gridDim.y) W *= 2;
+  const int sub = warp % W, rows_at_once = CNW / W;
   for (int r0 = blockIdx.y * rows_at_once; r0 < live; r0 += gridDim.y * rows_at_once) {
-    const int row = r0 + (many ? 0 : warp);
-    if (row >= live) break;  // (never where the block has barriers: there row is block-uniform)
+    const int row = r0 + warp / W;
     for (int e0 = 0; e0 < a.r; e0 += 256) {
       const int e = e0 + 4 * lane;  // and e + 128
-      const bool on0 = e < a.r, on1 = e + 128 < a.r;
+      const bool on0 = row < live && e < a.r, on1 = row < live && e + 128 < a.r;
       float M = -INFINITY, L = 0.f;
       float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-      for (int k0 = k_beg; k0 < parts; k0 += CNP * k_step) {
+      for (int k0 = sub; row < live && k0 < parts; k0 += CNP * W) {
         float2 ml[CNP];
         float4 o[CNP][2];
         float Mn = M;
 #pragma unroll
         for (int u = 0; u < CNP; ++u) {
-          const int k = k0 + u * k_step;
+          const int k = k0 + u * W;
           ml[u] = make_float2(-INFINITY, 0.f);
           o[u][0] = o[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k < parts) {
@@ -374,52 +423,53 @@ __global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_cons
 #pragma unroll
         for (int u = 0; u < CNP; ++u) {
           // (a part with nothing visible to this row holds no values of it)
-          const float g = exp2f(ml[u].x - ref);
-          if (!(g > 0.f)) continue;
-          L = fmaf(ml[u].y, g, L);
+          const float w = exp2f(ml[u].x - ref);
+          if (!(w > 0.f)) continue;
+          L = fmaf(ml[u].y, w, L);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            acc[h].x = fmaf(o[u][h].x, g, acc[h].x);
-            acc[h].y = fmaf(o[u][h].y, g, acc[h].y);
-            acc[h].z = fmaf(o[u][h].z, g, acc[h].z);
-            acc[h].w = fmaf(o[u][h].w, g, acc[h].w);
+            acc[h].x = fmaf(o[u][h].x, w, acc[h].x);
+            acc[h].y = fmaf(o[u][h].y, w, acc[h].y);
+            acc[h].z = fmaf(o[u][h].z, w, acc[h].z);
+            acc[h].w = fmaf(o[u][h].w, w, acc[h].w);
           }
         }
       }
-      if (many) {  // join the four warps' shares of the parts (block-uniform branch)
+      if (W > 1) {  // join the warps' shares of the parts (block-uniform branch)
         __syncthreads();
         red[warp][0][lane] = acc[0];
         red[warp][1][lane] = acc[1];
         if (lane == 0) red_ml[warp] = make_float2(M, L);
         __syncthreads();
-        if (warp != 0) continue;
-        float Mt = M;
-#pragma unroll
-        for (int w = 1; w < CNW; ++w) Mt = fmaxf(Mt, red_ml[w].x);
-        const float ref = Mt == -INFINITY ? 0.f : Mt, f = exp2f(M - ref);
-        M = Mt;
-        L *= f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
-        }
-#pragma unroll
-        for (int w = 1; w < CNW; ++w) {
-          const float g = exp2f(red_ml[w].x - ref);
-          L = fmaf(red_ml[w].y, g, L);
+        if (sub == 0) {
+          float Mt = M;
+          for (int w = 1; w < W; ++w) Mt = fmaxf(Mt, red_ml[warp + w].x);
+          const float ref = Mt == -INFINITY ? 0.f : Mt, f = exp2f(M - ref);
+          M = Mt;
+          L *= f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float4 o = red[w][h][lane];
-            acc[h].x = fmaf(o.x, g, acc[h].x);
-            acc[h].y = fmaf(o.y, g, acc[h].y);
-            acc[h].z = fmaf(o.z, g, acc[h].z);
-            acc[h].w = fmaf(o.w, g, acc[h].w);
+            acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+          }
+          for (int w = 1; w < W; ++w) {
+            const float2 ml = red_ml[warp + w];
+            const float g2 = exp2f(ml.x - ref);
+            L = fmaf(ml.y, g2, L);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 o = red[warp + w][h][lane];
+              acc[h].x = fmaf(o.x, g2, acc[h].x);
+              acc[h].y = fmaf(o.y, g2, acc[h].y);
+              acc[h].z = fmaf(o.z, g2, acc[h].z);
+              acc[h].w = fmaf(o.w, g2, acc[h].w);
+            }
           }
         }
       }
+      if (sub != 0) continue;
       const float inv = 1.f / L;
       const int64_t orow = row0 + row;
-      if (a.lse && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
+      if (a.lse && on0 && e == 0) a.lse[orow] = (M + log2f(L)) * 0.6931471805599453f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h == 0 ? !on0 : !on1) continue;
@@ -484,22 +534,28 @@ cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, int grid, int dtype, 
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int dtype, cudaStream_t st) {
+cudaError_t launch_paged_combine(const PagedAttnArgs& a, int grid, int sms, int dtype, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // a row a warp, of a long chunk two to four (the rows of an item: the tokens of
-  // an average sequence, all heads)
+  // As many blocks as are resident at once, up to one a row (of the average
+  // sequence's items).  An x for every block of the attention; where those leave
+  // too few y and items are far fewer, one for every item, which it then has to
+  // look for (1 us: fp32 chunks, 41 items in 296 blocks, 6.6 -> 3.3 us; 32 decode
+  // tokens in 148 blocks would take 1 us more).
+  const int64_t items = (a.c.N + a.plan.tpt - 1) / a.plan.tpt + a.c.B, most = items < a.c.N ? items : a.c.N;
   const int64_t item = (a.c.N + (int64_t)a.c.B - 1) / a.c.B * a.H, rows = item < a.rows ? item : a.rows;
-  const int64_t y = rows <= 8 ? rows : (rows <= 64 ? (rows + psimt::CNW - 1) / psimt::CNW : 16);
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)y);
+  const int64_t fit = 8 * (int64_t)sms;
+  const bool seek = fit / grid < rows && 4 * most <= grid;
+  const int64_t gx = seek ? most : grid, y = fit / gx < 1 ? 1 : (fit / gx < rows ? fit / gx : rows);
+  cfg.gridDim = dim3((unsigned)gx, (unsigned)y);
   cfg.blockDim = dim3(psimt::CNT);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return dtype == MTLA_BF16 ? cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<__nv_bfloat16>, a)
-                            : cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<float>, a);
+  return dtype == MTLA_BF16 ? cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<__nv_bfloat16>, a, seek ? grid : 0)
+                            : cudaLaunchKernelEx(&cfg, psimt::paged_combine_kernel<float>, a, seek ? grid : 0);
 }
 
 }  // namespace mtla
