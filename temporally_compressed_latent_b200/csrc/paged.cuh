@@ -280,9 +280,6 @@ __device__ __forceinline__ int64_t share_lo(int64_t C, int64_t G, int64_t x) {
   return C * x / G;
 }
 
-// With no more sequences than threads the plan keeps every sequence's window in
-// shared memory for the walk.
-constexpr int PLAN_WINS = 512;
 struct PlanShared {
   int64_t warp_sum[32];
   int64_t C, G, before;  // total weight; blocks with a share; weight of the sequences before `b`
@@ -306,9 +303,9 @@ __device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p,
 // Taken by every thread of the block: the total weight C, and the sequence
 // that holds position share_lo(C, G, x).  One pass over the sequences (each
 // thread sums a run of them) and one block scan; the thread whose run holds
-// the position walks its run again.  win: PLAN_WINS windows, kept where every
-// thread has one sequence at most.
-template <int NT>
+// the position walks its run again.  win: of no more than WINS <= NT sequences
+// the windows are kept here for the walk.
+template <int NT, int WINS>
 __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const PlanArgs& a, int grid, int x,
                                   int32_t* dev_err, PlanShared* sh, SeqWin* win) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -321,7 +318,7 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
     const SeqWin w = attn_win(c, p, a.div_s, b, x == 0 ? dev_err : nullptr);
     sum += seq_weight(a, w.t0, w.n);
     most = most > w.n ? most : w.n;
-    if (per == 1) win[b] = w;
+    if (c.B <= WINS) win[b] = w;
   }
   most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(most < a.tpt ? most : a.tpt));
   int64_t pre = sum;
@@ -344,7 +341,7 @@ __device__ inline void plan_block(const ChunkDev& c, const PagesDev& p, const Pl
   if (tid == 0) {
     sh->C = C;
     sh->G = G;
-    sh->kept = per == 1;
+    sh->kept = c.B <= WINS;
   }
   if (x < G) {
     const int64_t lo = share_lo(C, G, x);

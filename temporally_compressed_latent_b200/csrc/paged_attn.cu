@@ -26,11 +26,17 @@ namespace mtla {
 namespace psimt {
 
 constexpr int NT = 256;
+constexpr int WINS = 64;  // windows kept (the widest rows leave no more room)
 
 // key rows in shared memory: 4 elements more than the row, so that reads of 16
 // rows touch every bank group once
-__host__ __device__ inline int key_pitch(int D, int elem) { return (D + 16 / elem) * elem; }
-size_t smem_bytes(int D, int elem) { return (size_t)PSM * (D + 4) * 4 + (size_t)2 * PSN * key_pitch(D, elem) + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 + sizeof(PlanShared) + NT * sizeof(SeqWin) + sizeof(Item) + 64; }
+__host__ __device__ constexpr int key_pitch(int D, int elem) { return (D + 16 / elem) * elem; }
+constexpr size_t smem_bytes(int D, int elem) {
+  return (size_t)PSM * (D + 4) * 4 + (size_t)2 * PSN * key_pitch(D, elem) + (size_t)PSN * (PSM + 4) * 4 + PSM * 4 * 3 +
+         sizeof(PlanShared) + WINS * sizeof(SeqWin) + 32 * sizeof(ItemWalk) + sizeof(Item) + 64;
+}
+constexpr int MAXD = 576;  // r + d_R
+static_assert(smem_bytes(MAXD, 4) <= 232448, "the widest fp32 rows have to fit a block");
 
 template <typename T> __device__ __forceinline__ void ld4(const T* p, float* v);
 template <> __device__ __forceinline__ void ld4<float>(const float* p, float* v) {
@@ -73,9 +79,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 
 // NQ: channel quads per lane, ceil(r / 128); 0: r <= 64, where lanes 16 .. 31
-// take every second key
+// take every second key.  Three blocks an SM where the running output is small
+// (8 sequences of up to 33 tokens over 500 rows, r = 64: 19.1 us; two blocks
+// 21.7, four, whose registers spill, 21.9).
 template <typename T, int NQ0>
-__global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_attn_simt_kernel(const PagedAttnArgs a) {
   constexpr int NQ = NQ0 > 0 ? NQ0 : 1, NK = NQ0 > 0 ? 1 : 2;  // channel quads; key groups of a warp
   const int kg = NK == 2 ? (int)(threadIdx.x & 31) >> 4 : 0, cl = NK == 2 ? (int)threadIdx.x & 15 : (int)threadIdx.x & 31;
   extern __shared__ float smem[];
@@ -88,40 +96,38 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
   float* sm_a = sm_l + PSM;               // [PSM] rescale factors of the current tile
   PlanShared* plan = reinterpret_cast<PlanShared*>((reinterpret_cast<uintptr_t>(sm_a + PSM) + 15) & ~uintptr_t(15));
   SeqWin* wins = reinterpret_cast<SeqWin*>(plan + 1);
-  Item* sit = reinterpret_cast<Item*>(wins + NT);
+  ItemWalk* walks = reinterpret_cast<ItemWalk*>(wins + WINS);  // the first warp's, a lane each: no registers between items
+  Item* sit = reinterpret_cast<Item*>(walks + 32);
   int* more = reinterpret_cast<int*>(sit + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = gridDim.x, x = blockIdx.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_block<NT>(a.c, a.p, a.plan, grid, x, a.dev_err, plan, wins);
-  ItemWalk walk;
-  walk.hi = walk.pos = 0;
-  if (warp == 0) walk.init(a.c, a.p, a.plan, x, plan, wins);
-  SplitDesc desc = {0, 0, 0, 0, 0, 0};  // (warp 0)
+  plan_block<NT, WINS>(a.c, a.p, a.plan, grid, x, a.dev_err, plan, wins);
+  if (warp == 0) {
+    walks[lane].init(a.c, a.p, a.plan, x, plan, wins);
+    if (lane == 0) a.part.desc[x] = {0, 0, 0, 0, 0, 0};
+  }
 
   for (;;) {
     if (warp == 0) {
       Item it;
+      ItemWalk walk = walks[lane];
       const bool any = walk.next(a.c, a.p, a.plan, &it);
+      walks[lane] = walk;
       if (lane == 0) {
         *more = any;
         if (any) *sit = it;
       }
-      if (any && it.slot >= 0 && it.kt1 == it.kt) {  // a split item ends here
-        desc.row0 = it.row0;
-        desc.ntok = it.ntok;
-        desc.first = first_block(a.plan, walk.C, walk.G, walk.item_start);
-        desc.C = walk.C;
-        desc.G = walk.G;
-      }
+      if (any && it.slot >= 0 && it.kt1 == it.kt && lane == 0)  // a split item ends here
+        a.part.desc[x] = {it.row0, it.ntok, first_block(a.plan, walk.C, walk.G, walk.item_start), 0, walk.C, walk.G};
     }
     __syncthreads();
     if (!*more) break;
-    const Item it = *sit;
+    const Item& it = *sit;
     const int live = it.ntok * a.H;
-    const int64_t R8 = (it.R + 7) / 8 * 8;
+    const uint32_t R = (uint32_t)it.R, R8 = (R + 7) & ~7u;  // (below 2^31)
     if (tid < PSM) {
       sm_m[tid] = -INFINITY;
       sm_l[tid] = 0.f;
@@ -138,13 +144,13 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
     constexpr int RW = PSN / (NT / 32);           // rows a warp (4)
     const int chunks = D * (int)sizeof(T) / 16;   // 16-byte pieces of a row
     auto look = [&](int kt) -> int64_t {          // pool row, -1: zeros, or -2 - token: an own state
-      const int64_t g = (int64_t)kt * PSN + warp + (lane % RW) * (NT / 32);
-      if (g < it.R) {
+      const uint32_t g = (uint32_t)kt * PSN + warp + (lane % RW) * (NT / 32);
+      if (g < R) {
         const int64_t row = pool_row(a.p, it.b, g);
         if (row < 0) set_err(a.dev_err, MTLA_DEVERR_CAPACITY);
         return row;
       }
-      return g >= R8 && g - R8 < it.ntok ? -2 - (it.row0 + (g - R8)) : -1;
+      return g - R8 < (uint32_t)it.ntok ? -2 - (int64_t)it.row0 - (int64_t)(g - R8) : -1;
     };
     auto copy = [&](int64_t at, int buf) {
 #pragma unroll
@@ -184,17 +190,17 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
     // scores: this thread's rows r0, r0 + 16 (token, cache rows below it, virtual
     // row of its own state; a row past the live ones sees nothing)
     const int r0 = tid >> 4, c0 = tid & 15;
-    int64_t seen[2], own[2];
+    uint32_t seen[2], own[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int tok = (r0 + 16 * k) / a.H;
       seen[k] = tok < it.ntok ? rows_below(a.plan, it.t + tok) : 0;
-      own[k] = tok < it.ntok ? R8 + tok : -1;
+      own[k] = tok < it.ntok ? R8 + tok : 0xffffffffu;
     }
     int64_t ahead = it.kt0 + 1 < it.kt1 ? look(it.kt0 + 1) : -1;
 
     for (int kt = it.kt0; kt < it.kt1; ++kt) {
-      const int64_t v0 = (int64_t)kt * PSN;       // first virtual row
+      const uint32_t v0 = (uint32_t)kt * PSN;     // first virtual row
       const T* Ks = reinterpret_cast<const T*>(Kb + ((kt - it.kt0) & 1) * PSN * KP);
       if (kt + 1 < it.kt1) {
         copy(ahead, (kt + 1 - it.kt0) & 1);
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
       auto both = [](uint64_t v) { const float2 f = unpack2(v); return f.x + f.y; };
       const float s00 = both(t00), s01 = both(t01), s10 = both(t10), s11 = both(t11);
       auto put = [&](int k, int c, float v) {
-        const int64_t g = v0 + c;
+        const uint32_t g = v0 + c;
         Ss[c * (PSM + 4) + r0 + 16 * k] = g < seen[k] || g == own[k] ? v * a.scale_log2 : -INFINITY;
       };
       put(0, c0, s00);
@@ -324,7 +330,6 @@ __global__ void __launch_bounds__(NT) paged_attn_simt_kernel(const PagedAttnArgs
     }
     __syncthreads();  // the item and its statistics have been read
   }
-  if (tid == 0) a.part.desc[x] = desc;
 }
 
 // ----------------------------------------------------------------------------
@@ -506,7 +511,7 @@ int paged_simt_grid(int r, int d_R, int dtype, int sms) {
   if (last.dev == dev && last.r == r && last.d_R == d_R && last.dtype == dtype) return last.grid;
   auto k = dtype == MTLA_BF16 ? psimt::simt_kernel<__nv_bfloat16>(r) : psimt::simt_kernel<float>(r);
   int occ = 0;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psimt::smem_bytes(576, dtype == MTLA_BF16 ? 2 : 4)) != cudaSuccess)
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psimt::smem_bytes(psimt::MAXD, dtype == MTLA_BF16 ? 2 : 4)) != cudaSuccess)
     return 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, psimt::NT, psimt::smem_bytes(r + d_R, dtype == MTLA_BF16 ? 2 : 4)) != cudaSuccess ||
       occ < 1)

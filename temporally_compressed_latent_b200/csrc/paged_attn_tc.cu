@@ -62,6 +62,7 @@ constexpr int NSB = 4;                 // S / P buffers in TMEM (64 columns each
 __host__ __device__ constexpr uint32_t s_col(int b) { return 64u * (uint32_t)b; }
 constexpr uint32_t IDESC_O = umma_idesc_bf16(BM, R, false, true);
 constexpr int RING = 4;                // items in flight
+constexpr int WINS = NT;               // sequence windows kept
 constexpr int CONSUMERS = 3 + SMW + EPW;
 constexpr int OST_BYTES = 32 * 64;     // output staging of one epilogue warp: 32 rows x 64 bytes
 
@@ -77,12 +78,12 @@ constexpr size_t OFF_OST = OFF_K + (size_t)KS * KBYTES;
 constexpr size_t OFF_XCH = OFF_OST + (size_t)EPW * OST_BYTES;  // maxima [2][2][BM], sums [2][2][BM], final maxima [2][BM]
 constexpr size_t OFF_RING = OFF_XCH + 10 * BM * 4;
 constexpr size_t OFF_WIN = OFF_RING + RING * sizeof(RingItem);
-constexpr size_t OFF_PLAN = OFF_WIN + PLAN_WINS * sizeof(SeqWin);
+constexpr size_t OFF_PLAN = OFF_WIN + WINS * sizeof(SeqWin);
 constexpr size_t OFF_BAR = (OFF_PLAN + sizeof(PlanShared) + 15) / 16 * 16;
 constexpr int NBAR = 2 + 4 + 2 * (KS + 1) + 3 * NSB + 3 + 2 * RING;
 constexpr size_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr size_t SMEM = OFF_TMEM + 16 + 1024;
-static_assert(PLAN_WINS >= NT && OFF_WIN % 16 == 0, "a window a thread");
+static_assert(OFF_WIN % 16 == 0, "windows hold 64-bit fields");
 static_assert(QBYTES == 2 * KBYTES && OFF_Q == 0, "a stage in the queries' upper half");
 static_assert(OFF_K % 1024 == 0 && GRP % 512 == 0 && KBYTES % 1024 == 0, "swizzle atoms");
 static_assert(SMEM <= 232448, "one block's shared memory (227 KB)");
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   SeqWin* const wins = reinterpret_cast<SeqWin*>(sm + OFF_WIN);
   tc_fence_before();
-  plan_block<NT>(a.c, a.p, a.plan, gridDim.x, blockIdx.x, a.dev_err, plan, wins);  // (holds block barriers)
+  plan_block<NT, WINS>(a.c, a.p, a.plan, gridDim.x, blockIdx.x, a.dev_err, plan, wins);  // (holds block barriers)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t sQ = smem_u32(sm + OFF_Q);
