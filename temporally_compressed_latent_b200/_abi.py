@@ -132,9 +132,10 @@ def dims(H: int, d_h: int, r: int, d_R: int, s: int, dtype) -> _Dims:
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:  # an address
         return x
-    return x.data_ptr()
 
 
 def _stream(stream):
@@ -294,12 +295,13 @@ def mtla_paged_workspace_bytes(d, B, N, which) -> int:
 def _paged_stream(stream, dev_err):
     """The stream of a paged call.  Launches go to the current device: tensors of another one are refused
     (a stream given by the caller is taken as it is)."""
-    if stream is None and not isinstance(dev_err, int):
-        import torch
-        if dev_err.get_device() != torch.cuda.current_device():
-            raise ValueError(f"the call's tensors are on {dev_err.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    if stream is not None or isinstance(dev_err, int):
+        return _stream(stream)
+    import torch
+    dev = torch.cuda.current_device()
+    if dev_err.get_device() != dev:
+        raise ValueError(f"the call's tensors are on {dev_err.device}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)  # the handle without building a stream object
 
 
 def mtla_paged_append(d, B, chunk, merge, rope_base, q_rope, q_rope_out, cache, tail_in, tail_out, t_out, cache_len,

@@ -463,7 +463,6 @@ struct SplitDesc {
   int row0, ntok;   // ntok == 0: none
   int first;        // first block with a part of it
   int pad;
-  int64_t C, G;
 };
 // The first block that holds a key tile of an item at position `start`: the
 // last x with share_lo(x) <= start + item_cost.

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
   plan_block<NT, WINS>(a.c, a.p, a.plan, grid, x, a.dev_err, plan, wins);
   if (warp == 0) {
     walks[lane].init(a.c, a.p, a.plan, x, plan, wins);
-    if (lane == 0) a.part.desc[x] = {0, 0, 0, 0, 0, 0};
+    if (lane == 0) a.part.desc[x] = {0, 0, 0, 0};
   }
 
   for (;;) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
         if (any) *sit = it;
       }
       if (any && it.slot >= 0 && it.kt1 == it.kt && lane == 0)  // a split item ends here
-        a.part.desc[x] = {it.row0, it.ntok, first_block(a.plan, walk.C, walk.G, walk.item_start), 0, walk.C, walk.G};
+        a.part.desc[x] = {it.row0, it.ntok, first_block(a.plan, walk.C, walk.G, walk.item_start), 0};
     }
     __syncthreads();
     if (!*more) break;

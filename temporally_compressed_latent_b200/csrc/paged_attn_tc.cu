@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     // ======================= scheduler =======================
     ItemWalk walk;
     walk.init(a.c, a.p, a.plan, blockIdx.x, plan, wins);
-    SplitDesc desc = {0, 0, 0, 0, 0, 0};
+    SplitDesc desc = {0, 0, 0, 0};
     for (uint32_t n = 0;; ++n) {
       Item item;
       const bool any = walk.next(a.c, a.p, a.plan, &item);
@@ -238,8 +238,6 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         desc.row0 = item.row0;
         desc.ntok = item.ntok;
         desc.first = first_block(a.plan, walk.C, walk.G, walk.item_start);
-        desc.C = walk.C;
-        desc.G = walk.G;
       }
     }
     if (lane == 0) a.part.desc[blockIdx.x] = desc;
