@@ -19,8 +19,8 @@
 //    through a ring in shared memory, so no warp reads the sequence arrays on
 //    its own path.  Parts of items that a share boundary splits go to the
 //    workspace in fp32 and a second kernel joins them.
-//  * Three key tiles in flight, or four where no item has more than 64 live
-//    rows: the fourth then lies in the upper half of the queries' space.  A
+//  * Three key tiles in flight, four where no item has more than 64 live rows and
+//    five where none has more than 40 (the queries' groups leave that room).  A
 //    stage is free again only after its value MMA, about 2.3 us after it landed
 //    (score MMA, softmax, value MMA), so three stages gave 1.07 us a tile to a
 //    decode step.
@@ -52,7 +52,7 @@ constexpr int BN = 64;                 // columns of a key tile
 constexpr int GRP = D / 32 * 512;      // bytes of an 8-row group: nine planes of 8 x 64 B (4608)
 constexpr int QBYTES = BM / 8 * GRP;   // 73728
 constexpr int KBYTES = BN / 8 * GRP;   // 36864
-constexpr int KS = 3;                  // key-tile stages, and one more where queries take half their space
+constexpr int KS = 5;                  // key-tile stages at most
 constexpr int SMW = 8, EPW = 4;        // softmax and epilogue warps
 constexpr int TMA_WARP = SMW, SMMA_WARP = SMW + 1, PMMA_WARP = SMW + 2, SCHED_WARP = SMW + 3, EPI_WARP0 = SMW + 4;
 constexpr int NT = 32 * (SMW + 4 + EPW);
@@ -73,19 +73,28 @@ struct RingItem {
 };
 
 constexpr size_t OFF_Q = 0;
-constexpr size_t OFF_K = OFF_Q + QBYTES;
-constexpr size_t OFF_OST = OFF_K + (size_t)KS * KBYTES;
+// Operands: the queries' groups and as many key stages as lie behind those that
+// can be live: five behind 40 rows, four behind 64, three behind all 128 (the
+// score MMA always reads the place of all 128: what stands in a dead row's
+// groups, keys among them, ends in a dead row's scores).
+constexpr int Q5_ROWS = 40;
+constexpr size_t OPERANDS = Q5_ROWS / 8 * GRP + (size_t)KS * KBYTES;
+__host__ __device__ constexpr int stages_of(int rows) { return rows <= Q5_ROWS ? 5 : (rows <= BM / 2 ? 4 : 3); }
+__host__ __device__ constexpr uint32_t keys_off(int stages) {
+  return stages == 5 ? Q5_ROWS / 8 * GRP : (stages == 4 ? QBYTES / 2 : QBYTES);
+}
+static_assert(keys_off(4) + 4 * KBYTES <= OPERANDS && keys_off(3) + 3 * KBYTES <= OPERANDS, "stages");
+constexpr size_t OFF_OST = OPERANDS;
 constexpr size_t OFF_XCH = OFF_OST + (size_t)EPW * OST_BYTES;  // maxima [2][2][BM], sums [2][2][BM], final maxima [2][BM]
 constexpr size_t OFF_RING = OFF_XCH + 10 * BM * 4;
 constexpr size_t OFF_WIN = OFF_RING + RING * sizeof(RingItem);
 constexpr size_t OFF_PLAN = OFF_WIN + WINS * sizeof(SeqWin);
 constexpr size_t OFF_BAR = (OFF_PLAN + sizeof(PlanShared) + 15) / 16 * 16;
-constexpr int NBAR = 2 + 4 + 2 * (KS + 1) + 3 * NSB + 3 + 2 * RING;
+constexpr int NBAR = 2 + 4 + 2 * KS + 3 * NSB + 3 + 2 * RING;
 constexpr size_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr size_t SMEM = OFF_TMEM + 16 + 1024;
 static_assert(OFF_WIN % 16 == 0, "windows hold 64-bit fields");
-static_assert(QBYTES == 2 * KBYTES && OFF_Q == 0, "a stage in the queries' upper half");
-static_assert(OFF_K % 1024 == 0 && GRP % 512 == 0 && KBYTES % 1024 == 0, "swizzle atoms");
+static_assert(OFF_Q == 0 && GRP % 512 == 0 && KBYTES % 512 == 0 && OFF_OST % 512 == 0, "64-byte swizzle: atoms of 512 bytes");
 static_assert(SMEM <= 232448, "one block's shared memory (227 KB)");
 
 // 2^x with the hardware approximation (relative error about 2^-22; 2^-inf = 0)
@@ -128,9 +137,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   uint64_t* const q_empty = bar + 1;            // the item's last score MMA has read Q
   uint64_t* const stat_full = bar + 2;          // [2] an item's row maxima and sums are written
   uint64_t* const stat_empty = bar + 4;         // [2] the epilogue has read them
-  uint64_t* const k_full = bar + 6;             // [KS + 1]
-  uint64_t* const k_empty = k_full + KS + 1;    // [KS + 1]
-  uint64_t* const s_full = k_empty + KS + 1;    // [NSB]
+  uint64_t* const k_full = bar + 6;             // [KS]
+  uint64_t* const k_empty = k_full + KS;        // [KS]
+  uint64_t* const s_full = k_empty + KS;        // [NSB]
   uint64_t* const p_full = s_full + NSB;        // [NSB]
   uint64_t* const p_empty = p_full + NSB;       // [NSB] the value MMA has read P
   uint64_t* const o_full = p_empty + NSB;
@@ -153,7 +162,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       mbar_init(&stat_full[i], SMW);
       mbar_init(&stat_empty[i], EPW);
     }
-    for (int i = 0; i < KS + 1; ++i) {
+    for (int i = 0; i < KS; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
@@ -191,8 +200,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   const uint32_t sQ = smem_u32(sm + OFF_Q);
   const int H = a.H;
   // key-tile stages: number, and the place of each
-  const uint32_t ns = plan->most * H <= BM / 2 ? KS + 1 : KS;
-  auto stage_off = [](uint32_t st) -> uint32_t { return st < (uint32_t)KS ? (uint32_t)OFF_K + st * KBYTES : (uint32_t)OFF_Q + QBYTES / 2; };
+  const uint32_t ns = stages_of(plan->most * H), k_off = keys_off(ns);
+  auto stage_off = [k_off](uint32_t st) -> uint32_t { return k_off + st * KBYTES; };
   bool ok = true;
 
   // the next item of the block's share, for one consumer warp
