@@ -23,11 +23,12 @@
 //    leave P rows, pool rows, positions and bit masks (which tokens open a
 //    group, end a chunk, ...) in shared memory, and send the tile's P rows
 //    towards L2.  The epilogue's 12 warps take 32 columns each in chunks of 8
-//    (2048 tokens of four prompts, 32 query rows a token, on B200: 32.3 us; of
-//    16 columns 33.0, whose longer code no longer stays in the instruction
-//    cache; of 4 35.2).  They are bound by issue and by the latency of their
-//    chain, so P comes to shared memory by asynchronous copies while the tile before is stored, and
-//    finished rows leave through a staging block, 16 bytes of eight rows a step.
+//    (8 prompt chunks, 23,000 tokens, s = 2: 32.2 us, 1.87 TB/s of what has to
+//    move; of 16 columns 33.0, whose longer code misses the instruction cache
+//    more; of 4 35.2).  They are bound by issue and by the latency of their
+//    chain, so P comes to shared memory by asynchronous copies while the tile
+//    before is stored, and finished rows leave through a staging block, 16 bytes
+//    of eight rows a step.
 //  * RoPE: an exact angle every 8 tokens of a run of positions and a rotation
 //    by the pair's own angle between them (at most seven single-precision
 //    products: error below 2^-20 of the key).
