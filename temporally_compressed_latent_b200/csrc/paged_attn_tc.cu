@@ -23,7 +23,8 @@
 //    five where none has more than 40 (the queries' groups leave that room).  A
 //    stage is free again only after its value MMA, about 2.3 us after it landed
 //    (score MMA, softmax, value MMA), so three stages gave 1.07 us a tile to a
-//    decode step.
+//    decode step; 128 sequences of up to 5 tokens and 8 heads took 57.9 us with
+//    four and 55.8 with five.
 //  * Tiles are lists of 8-row groups: a group is nine [8 x 64 B] planes with the
 //    64-byte swizzle (4608 bytes, one TMA box), so a page of any multiple of 8
 //    rows feeds a key tile, the operand's 8-row stride is 4608 everywhere, and
@@ -41,6 +42,10 @@
 //    operand.  A score warp and a value warp issue them; eight softmax warps,
 //    two a lane quarter, rescale O only when a row's maximum grows by more
 //    than 2^8; four epilogue warps store an item while the next one starts.
+//  Measured (s = 2, H = 8): 32 single tokens over 2048 rows 20.2 us (1.88 TB/s;
+//  seven tiles a block between fixed 13 us), 128 sequences of up to 5 tokens over
+//  2048 .. 4096 rows 55.8 us (4.05 TB/s), four chunks of 1024 tokens after 16384
+//  283 us (1064 TFLOP/s).
 #include "paged.cuh"
 
 namespace mtla {
