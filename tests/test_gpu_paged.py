@@ -231,6 +231,39 @@ def test_attention_shapes(new, past, kw):
     assert int(b.err.item()) == 0
 
 
+def _some(b, k=60):
+    """Every sequence's first and last token and some others."""
+    every = [(i, j) for i in range(b.B) for j in range(b.take[i])]
+    ends = {(i, j) for i in range(b.B) if b.take[i] for j in (0, b.take[i] - 1)}
+    rng = np.random.default_rng(1)
+    more = [every[i] for i in rng.choice(len(every), min(k, len(every)), replace=False)]
+    return sorted(ends | set(more))
+
+
+@pytest.mark.parametrize("most", [1, 5, 6, 8, 9, 16])
+def test_attention_live_rows(most):
+    """Chunks whose items hold 8 to 128 live rows, over more key tiles than are in flight."""
+    b = Batch([most, 1, most, 2], [1500, 3, 700, 2900], s=1, page_rows=16, seed=most)
+    b.fill_groups()
+    b.check_attn(b.attn(), tokens=_some(b))
+    assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("new,past,kw", [
+    ([33, 33, 9], [3000, 2000, 50], dict(s=1)),                  # few items, each in many parts
+    ([1], [4000], dict(s=1)),                                    # one row of them
+    ([300, 2], [900, 5000], dict(s=2)),                          # a sequence of more items than are added one by one
+    ([1 + i % 3 for i in range(100)], [(37 * i) % 300 for i in range(100)], dict(s=3)),  # more windows than are kept
+], ids=["few", "one", "items", "sequences"])
+@pytest.mark.parametrize("dims", [TINY, WIDE32], ids=["tiny", "wide32"])
+def test_attention_parts(new, past, kw, dims):
+    """The generic kernel's shares and the joining of their parts."""
+    b = Batch(new, past, page_rows=8, seed=17, **kw, **dims)
+    b.fill_groups()
+    b.check_attn(b.attn(), tokens=_some(b))
+    assert int(b.err.item()) == 0
+
+
 def test_attention_options():
     kw = dict(new=[4, 19, 3, 2], past=[3, 900, 0, 130], s=2, page_rows=8, seed=3)
     b = Batch(pad=8, **kw)
@@ -360,6 +393,24 @@ def test_verify_many_drafts():
             ua[drop] = 1.5
         keep, nxt, _ = _verify(p, q, tokens, [0, n], ua, [0.4])
         assert (keep, nxt) == verify_ref(p, q, tokens, [0, n], ua, [0.4]) and keep == [(n if drop is None else drop + 1)]
+
+
+@pytest.mark.parametrize("V,lens", [
+    (20001, [3, 1] * 40),                     # more sequences than can have eight blocks each at once
+    (1 << 22, [2] + [0] * 59),                # the largest vocabulary, with four blocks a sequence
+    (1 << 22, [2]),                           # and with eight
+], ids=["many", "widest4", "widest8"])
+def test_verify_blocks(V, lens):
+    rng = np.random.default_rng(V + len(lens))
+    start = np.concatenate([[0], np.cumsum(lens)])
+    N = int(start[-1])
+    p, q = _dists(rng, N, V)
+    tokens = rng.integers(0, V, N)
+    for us in (rng.random(len(lens)), np.full(len(lens), 0.999999)):
+        for Q in (q, None):
+            ua, u = rng.random(N).astype(np.float32), us.astype(np.float32)
+            keep, nxt, err = _verify(p, Q, tokens, start, ua, u)
+            assert (keep, nxt) == verify_ref(p, Q, tokens, start, ua, u) and err == 0
 
 
 def test_verify_odd_distributions():
