@@ -163,6 +163,7 @@ __device__ __forceinline__ float2 rope_cos_sin(uint32_t pos, uint64_t turns) {
 struct PlanArgs {
   int s, tpt, q, item_cost;
   int min_share;   // least weight worth a block of its own
+  int one_block;   // most weight that one block takes alone
   FastDiv div_s;
 };
 // sum over i in [0, n) of floor((a i + b) / m), by the Euclidean recursion
@@ -201,7 +202,7 @@ __device__ __forceinline__ int item_tiles(const PlanArgs& a, int64_t t, int k) {
 constexpr int ADD_ITEMS = 32;
 static __device__ __noinline__ int64_t items_weight_many(int s, int tpt, int q, int item_cost, FastDiv div_s, int64_t t0, int n,
                                                          int64_t m) {
-  const PlanArgs a = {s, tpt, q, item_cost, 0, div_s};
+  const PlanArgs a = {s, tpt, q, item_cost, 0, 0, div_s};
   int64_t w = m * a.item_cost;
   if (m <= ADD_ITEMS) {
     for (int i = 0; i < (int)m; ++i) {
@@ -259,18 +260,21 @@ struct Item {
 // An upper bound of the blocks that get a share, from what the host knows (N
 // tokens of B sequences, tables of `rows` cache rows).  Where it is one, no item
 // is split and nothing is left to join.
+inline int64_t most_tiles(const PlanArgs& a, int64_t N, int64_t rows) {  // of an item
+  return ((rows + 7) / 8 + ((a.tpt < N ? a.tpt : N) + 7) / 8 + a.q - 1) / a.q;
+}
 inline int most_blocks(const PlanArgs& a, int64_t N, int64_t B, int64_t rows, int grid) {
   int64_t items = (N + a.tpt - 1) / a.tpt + B;
   if (items > N) items = N;
-  const int64_t tiles = ((rows + 7) / 8 + (a.tpt + 7) / 8 + a.q - 1) / a.q, C = items * (a.item_cost + tiles);
-  if (C <= 2 * a.min_share) return 1;
+  const int64_t C = items * (a.item_cost + most_tiles(a, N, rows));
+  if (C <= a.one_block) return 1;
   const int64_t g = (C + a.min_share - 1) / a.min_share;
   return g < grid ? (int)g : grid;
 }
 // Blocks that get a share: no more than give each min_share of the weight C.
 __device__ __forceinline__ int64_t share_blocks(const PlanArgs& a, int64_t C, int grid) {
   if (C >= (int64_t)a.min_share * grid) return grid;
-  if (C <= 2 * a.min_share) return C > 0;  // too little to pay for joining parts
+  if (C <= a.one_block) return C > 0;  // too little to pay for joining parts
   return ((int)C + a.min_share - 1) / a.min_share;
 }
 // Shares: block x of G takes [C x / G, C (x + 1) / G).

@@ -230,10 +230,18 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   a.plan.s = dims->s;
   a.plan.tpt = tpt < 16 ? tpt : 16;
   a.plan.q = (sh.tc ? PTC_COLS : PSN) / 8;
-  a.plan.item_cost = 2;
-  a.plan.min_share = sh.tc ? 4 : 1;
+  // An item costs about three key tiles to start and to store; a share of its own
+  // pays from about that weight on, and joining from twice as much (tensor cores:
+  // 14 sequences of one tile 10.0 us with shares of 3, 11.8 with 4, 10.0 with 2;
+  // 1694 tokens of short sequences 29.6 with a cost of 3, 33.5 with 2; generic
+  // kernel: one token of one tile 8.6 alone, 9.8 joined; two sequences of 17 tokens
+  // 12.7 with shares of 1, 16.8 with 2).
+  a.plan.item_cost = 3;
+  a.plan.min_share = sh.tc ? 3 : 1;
+  a.plan.one_block = sh.tc ? 8 : 6;
   a.plan.div_s = fast_div((uint32_t)dims->s);
-  const int grid = most_blocks(a.plan, chunk->N, B, (int64_t)cache->table_pages * cache->page_rows, sh.grid);
+  const int64_t rows = (int64_t)cache->table_pages * cache->page_rows;
+  const int grid = most_blocks(a.plan, chunk->N, B, rows, sh.grid);
   if (sh.tc) {
     PagedAttnMaps maps;
     if (!paged_maps(&maps, a)) return MTLA_ERR_CUDA;
@@ -241,7 +249,9 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   } else if (launch_paged_attn_simt(a, grid, dims->dtype, cs) != cudaSuccess) {
     return MTLA_ERR_CUDA;
   }
-  return grid > 1 ? from_cuda(launch_paged_combine(a, grid, current_device_sms(), dims->dtype, cs)) : MTLA_OK;
+  // nothing to join where one block takes all, or no item has two tiles
+  if (grid == 1 || most_tiles(a.plan, chunk->N, rows) <= 1) return MTLA_OK;
+  return from_cuda(launch_paged_combine(a, grid, current_device_sms(), dims->dtype, cs));
 }
 
 mtla_status mtla_verify_drafts(int32_t B, int32_t N, int32_t V, const float* p, int64_t ld_p, const float* q,
