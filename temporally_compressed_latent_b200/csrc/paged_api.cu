@@ -104,9 +104,9 @@ void rope_table(double base, int d_R, RopeTable* t) {
 // The append's tensor-core kernel: the widths its tiles are laid out for, groups
 // that fit beside half a tile, and enough tokens that its start (W_c into TMEM,
 // metadata) costs less than the generic kernel's arithmetic.  Generic against
-// tensor cores, us: one sequence of 448 tokens 8.6 / 11.5, of 512 13.9 / 11.2,
-// of 1024 20.7 / 11.3; one token of 256 sequences 10.2 / 17.5, of 512 17.9 /
-// 17.9, of 1024 26.7 / 18.2.
+// tensor cores, us: one sequence of 384 tokens 8.6 / 10.2, of 512 13.8 / 10.1, of
+// 1024 20.7 / 10.5; one token of 256 sequences 10.2 / 15.0, of 512 18.2 / 15.4, of
+// 1024 26.8 / 15.7.
 constexpr int APPEND_TC_TOKENS = 512;
 bool append_tc(const mtla_dims* d, int32_t N) {
   return d->dtype == MTLA_BF16 && d->r == 256 && d->d_R == 32 && d->s <= PTA_MAX_S && N >= APPEND_TC_TOKENS;

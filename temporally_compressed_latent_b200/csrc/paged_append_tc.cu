@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(QT, 4) paged_rotate_kernel(const __grid_consta
 }
 
 __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ PagedAppendMaps mp,
-                                                                const __grid_constant__ PagedAppendArgs a, int n_tiles) {
+                                                                const __grid_constant__ PagedAppendArgs a, int n_tiles, int cols) {
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not an integer address: the compiler keeps seeing shared memory)
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -198,7 +198,7 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
   const int ct = blockIdx.x % CT, G = gridDim.x / CT, j0 = blockIdx.x / CT;
   const int u_beg = (int)((int64_t)j0 * n_tiles / G), u_end = (int)((int64_t)(j0 + 1) * n_tiles / G);
   const bool has_rope = (ct + 1) * NCT > R;
-  const int s = a.s, halo = s - 1, nout = NTOK - halo;
+  const int s = a.s, halo = s - 1, nout = cols - halo;  // columns in use; tokens of a tile
   const int q = warp & 3, part = warp >> 2;      // TMEM lane quarter; eighth of the tile's columns
   const bool epi = q < 3;
   const int ch = ct * NCT + q * 32 + lane;       // this thread's channel (epilogue warps)
@@ -452,7 +452,7 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
       const Meta& mt = meta[ab];
       // this warp's columns [cb, ce) of [p0, p0 + PCOL); masks are bits of the column in its word of 32
       const int cb = p0 > halo ? p0 : halo;
-      const int64_t lastc = a.c.N - base;        // columns past it are no token rows
+      const int64_t lastc = a.c.N - base < cols ? a.c.N - base : cols;  // columns past it are no token rows, or the next tile's
       const int ce = p0 + PCOL < lastc ? p0 + PCOL : (int)lastc;
       if (cb < ce) {
         const uint32_t vrow = rope ? smem_u32(sm + OFF_KR + ab * KRBLK) + (uint32_t)(lane >> 1) * 4 : sB + (sb + c_kb) * BBLK + c_in;
@@ -627,8 +627,14 @@ cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMa
     if (e != cudaSuccess) return e;
     if (dev < 64) done_mask |= 1ull << dev;
   }
-  const int n_tiles = (int)cdiv(a.c.N, ptp::NTOK - (a.s - 1));
   int per = sms / ptp::CT > 0 ? sms / ptp::CT : 1;  // CTAs per channel tile
+  // The fewest columns (a warp's part each) that give no CTA a second tile, unless
+  // the first s - 1 would be half of them: a scheduler then serves fewer warps
+  // (four tokens of 128 sequences 13.0 us, with 128 columns 15.3; one of 512
+  // 15.6 / 18.0; one sequence of 1024 10.5 / 11.2).
+  int cols = ptp::PCOL;
+  while (cols < ptp::NTOK && (cols < 2 * (a.s - 1) || cdiv(a.c.N, cols - (a.s - 1)) > per)) cols += ptp::PCOL;
+  const int n_tiles = (int)cdiv(a.c.N, cols - (a.s - 1));
   if (n_tiles < per) per = n_tiles;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -640,7 +646,7 @@ cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMa
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, ptp::paged_append_tc_kernel, m, a, n_tiles);
+  e = cudaLaunchKernelEx(&cfg, ptp::paged_append_tc_kernel, m, a, n_tiles, cols);
   if (e != cudaSuccess || !a.q_rope) return e;
   cfg.gridDim = dim3((unsigned)cdiv(a.c.N, ptp::QT / 32 * ptp::QROWS));
   cfg.blockDim = dim3(ptp::QT);
