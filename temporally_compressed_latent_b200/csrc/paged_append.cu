@@ -21,8 +21,8 @@
 // whether needed or not, and no read waits to know) and the sequences' windows
 // are all requested at the start, and P, the tails, the RoPE keys and the table
 // entries as soon as the windows are known, before the products.  One token takes
-// 4.4 us (of which a launch is 2 to 3), one token of 32 sequences 7.5 us, 24 fp32
-// sequences of 5 drafts 5.4 us.
+// 4.4 us (of which a launch is 2 to 3), one token of 32 sequences 5.5 us, 24 fp32
+// sequences of 5 drafts 4.1 us.
 #include "paged.cuh"
 
 namespace mtla {
@@ -30,6 +30,7 @@ namespace pap {
 
 constexpr int NT = 256, NW = NT / 32;
 constexpr int U = 16;                // tokens of one round
+constexpr int RESIDENT = 2;          // blocks an SM
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
@@ -288,15 +289,24 @@ static auto pick(int r) -> void (*)(const PagedAppendArgs, int, int) {
 cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cudaStream_t st) {
   const int D = a.r + a.d_R, slabs = (D + 31) / 32;
   // Tile length: one round of 16 tokens while that does not give every SM its
-  // eight blocks, then longer (W_c is read once a block).  A stride of up to 9
-  // takes the s - 1 rows before a tile into its rounds; with a longer one the
-  // tile is not below the stride, up to 512 tokens, so that it recomputes at
-  // most about its own length again.
+  // eight blocks, then longer (W_c is read once a block); of fewer tokens where all
+  // blocks then start at once and no more than two thirds of its rows are those
+  // before it (one token of 32 sequences 5.5 us, in rounds of 16 7.6; four tokens
+  // of 44 sequences 7.2, of 16 9.1, of 4 in more blocks than start at once 11.0).
+  // A stride of up to 9 takes the s - 1 rows before a tile into its rounds; with a
+  // longer one the tile is not below the stride, up to 512 tokens, so that it
+  // recomputes at most about its own length again.
   int64_t rounds = cdiv((int64_t)a.c.N * slabs, (int64_t)pap::U * sms * 8);
   rounds = rounds < 1 ? 1 : (rounds > 16 ? 16 : rounds);
   int64_t tt = rounds * pap::U;
   if (a.s <= 9) {
     a.halo = a.s - 1;
+    if (rounds == 1)
+      for (int few = 4; few < pap::U; few += 4)
+        if (2 * few >= 3 * a.halo && cdiv(a.c.N, few - a.halo) * slabs <= (int64_t)sms * pap::RESIDENT) {
+          tt = few;
+          break;
+        }
     tt -= a.halo;
   } else {
     a.halo = -1;
