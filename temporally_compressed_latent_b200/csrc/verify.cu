@@ -7,7 +7,7 @@
 // all are kept, from p of the chunk's last row.  It is drawn by inversion: the
 // lowest index whose running sum exceeds u times the sum.
 //
-// A cluster of up to 8 blocks takes a sequence: only one row of p and of q is
+// A cluster of up to 16 blocks takes a sequence: only one row of p and of q is
 // read (the drafts' probabilities are gathers), so the vocabulary is split over
 // the cluster for its latency and bandwidth, and the blocks exchange their sums
 // through distributed shared memory.  A warp sums 256 entries at a time, eight
@@ -30,7 +30,7 @@ namespace mtla {
 namespace vfy {
 
 namespace cg = cooperative_groups;
-constexpr int MAXCL = 8;
+constexpr int MAXCL = 16;
 constexpr int NT = 256, NW = NT / 32, BLOCKS = 3;   // threads; resident blocks an SM (of 4, 64 registers spill: 96 x 131072 2.5 us longer)
 constexpr int RUN = 256;                            // entries a warp sums at a time
 constexpr int MAXRUNS = 4104;                       // runs of a block (2^22 entries over 4 blocks: 4097)
@@ -284,15 +284,27 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
 }  // namespace vfy
 
 cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
-  // A block of the cluster per 4096 entries, up to 8, or up to 4 where 8 a
-  // sequence would not all be resident: one sequence of 32000 entries takes 6.2 us
-  // with 4 blocks and 5.5 with 8; 96 of 131072 take 21.2 with 4 (23.2 with 3) and
-  // 25.0 with 8, whose last clusters start when the first are through.  With small
-  // vocabularies more blocks would only wait.  (4 or 8 also keep a block's notes
-  // within its shared memory.)
-  const int most = (int64_t)a.B * vfy::MAXCL > (int64_t)vfy::BLOCKS * sms ? vfy::MAXCL / 2 : vfy::MAXCL;
+  // A block of the cluster per 4096 entries, up to 16, or 8 or 4 where more a
+  // sequence would not all be resident: 5 sequences of 123745 entries take 9.3 us
+  // with 8 blocks and 7.5 with 16, one of 32000 6.2 with 4 and 5.6 with 8; 96 of
+  // 131072 take 21.2 with 4 (23.2 with 3) and 25.0 with 8, whose last clusters
+  // start when the first are through.  With small vocabularies more blocks would
+  // only wait.  (Four or more also keep a block's notes within its shared memory.)
+  int most = vfy::MAXCL;
+  while (most > 4 && (int64_t)a.B * most > (int64_t)vfy::BLOCKS * sms) most /= 2;
   int cl = (a.V + 4095) / 4096;
   cl = cl < most ? cl : most;
+  if (cl > 8) {  // past the portable size: allowed once per device
+    static uint64_t done_mask = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done_mask & (1ull << dev))) {
+      e = cudaFuncSetAttribute(vfy::verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) done_mask |= 1ull << dev;
+    }
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cl;

@@ -398,8 +398,9 @@ def test_verify_many_drafts():
 @pytest.mark.parametrize("V,lens", [
     (20001, [3, 1] * 40),                     # more sequences than can have eight blocks each at once
     (1 << 22, [2] + [0] * 59),                # the largest vocabulary, with four blocks a sequence
-    (1 << 22, [2]),                           # and with eight
-], ids=["many", "widest4", "widest8"])
+    (1 << 22, [1] + [0] * 39 + [2]),          # with eight
+    (1 << 22, [2]),                           # and with sixteen
+], ids=["many", "widest4", "widest8", "widest16"])
 def test_verify_blocks(V, lens):
     rng = np.random.default_rng(V + len(lens))
     start = np.concatenate([[0], np.cumsum(lens)])
