@@ -231,14 +231,15 @@ mtla_status mtla_paged_attn(const mtla_dims* dims, int32_t B, const mtla_chunk* 
   a.plan.tpt = tpt < 16 ? tpt : 16;
   a.plan.q = (sh.tc ? PTC_COLS : PSN) / 8;
   // An item costs about three key tiles to start and to store; a share of its own
-  // pays from about that weight on, and joining from twice as much (tensor cores:
+  // pays from about that weight on, and joining from somewhat more (tensor cores:
   // 14 sequences of one tile 10.0 us with shares of 3, 11.8 with 4, 10.0 with 2;
-  // 1694 tokens of short sequences 29.6 with a cost of 3, 33.5 with 2; generic
-  // kernel: one token of one tile 8.6 alone, 9.8 joined; two sequences of 17 tokens
-  // 12.7 with shares of 1, 16.8 with 2).
+  // 1694 tokens of short sequences 29.6 with a cost of 3, 33.5 with 2; one sequence
+  // of six tiles joined 12.1, in one block 13.0.  Generic kernel: two sequences of
+  // 17 tokens 12.7 with shares of 1, 16.8 with 2; one token of one tile 8.7 alone
+  // and 9.8 joined, of two 12.1 and 10.7).
   a.plan.item_cost = 3;
   a.plan.min_share = sh.tc ? 3 : 1;
-  a.plan.one_block = sh.tc ? 8 : 6;
+  a.plan.one_block = sh.tc ? 8 : 4;
   a.plan.div_s = fast_div((uint32_t)dims->s);
   const int64_t rows = (int64_t)cache->table_pages * cache->page_rows;
   const int grid = most_blocks(a.plan, chunk->N, B, rows, sh.grid);
