@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(NT, BLOCKS) verify_kernel(const VerifyArgs a) 
   __shared__ double warp_total[NW];
   __shared__ double totals[2][MAXCL];                 // every block's sum, written by the blocks themselves
   __shared__ int first_drop;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / CL;
 
@@ -305,16 +307,18 @@ cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
       if (dev < 64) done_mask |= 1ull << dev;
     }
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cl;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.B * (unsigned)cl);
   cfg.blockDim = dim3(vfy::NT);
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, vfy::verify_kernel, a);
 }
 
