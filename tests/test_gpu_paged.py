@@ -337,6 +337,83 @@ def test_attention_equals_the_contiguous_decode():
     assert (out - o["out"]).abs().max().item() <= 2 * 2.0 ** -8 * float(buf.float().abs().max())
 
 
+# ------------------------------------------------- offsets past 32 bits
+
+
+def _behind(x, off):
+    """x's rows behind off others."""
+    big = torch.empty((off + x.shape[0],) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+    big[off:] = x
+    return big
+
+
+@pytest.fixture
+def freed():
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dims", [{}, TINY], ids=["main", "tiny"])
+def test_far_pages(dims, freed):
+    """Pages more than 2^31 elements into the pool."""
+    for call in ("append", "attn"):
+        width = dims.get("r", 256) + dims.get("d_R", 32)
+        b = Batch([3, 1, 40], [100, 0, 601], s=2, page_rows=16, pad=16384 - width, seed=23, **dims)
+        if call == "attn":
+            b.fill_groups()
+        first = (1 << 31) // (16 * 16384) + 1
+        pool = _behind(b.d_pages, first)
+        table = torch.where(b.d_table >= 0, b.d_table + first, b.d_table)
+        b.paged = mtla.paged_cache(pool, first + b.num_pages, 16, b.stride, table, b.table_pages)
+        o = getattr(b, call)()
+        if call == "append":
+            torch.cuda.synchronize()
+            b.d_pages.copy_(pool[first:])
+            b.check_append(o)
+        else:
+            b.check_attn(o)
+        assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("dims", [{}, TINY], ids=["main", "tiny"])
+def test_far_tokens(dims, freed):
+    """Tokens more than 2^31 elements into every token array, behind a sequence of which none is taken."""
+    i32 = lambda v: torch.tensor(np.asarray(v, np.int32), device="cuda")
+    b = Batch([3, 1, 40], [100, 0, 601], s=2, page_rows=16, seed=29, **dims)
+    table = torch.cat([torch.zeros_like(b.d_table[:1]), b.d_table])
+    paged = mtla.paged_cache(b.d_pages, b.num_pages, b.pr, b.stride, table, b.table_pages)
+    row = lambda x: torch.cat([x[:1], x])          # the sequence in front
+
+    def chunk(off):
+        N = off + b.N
+        return N, mtla.chunk(N, i32([0] + [off + x for x in b.start]), i32([0] + b.past), i32([0] + b.take))
+
+    off = (1 << 31) // b.r + 5
+    N, c = chunk(off)
+    m = mtla.merge_args(_behind(b.d["c"], off), _behind(b.d["kR"], off), b.d["W_c"], b.d["b_c"], b.d["P"], b.d["P"].shape[0])
+    state, q = (_behind(torch.full_like(b.d[k], float("nan")), off) for k in ("state", "q_rope"))
+    tail = torch.full((b.B + 1, b.D), float("nan"), device="cuda")
+    t, n = i32([-5] * (b.B + 1)), i32([-5] * (b.B + 1))
+    tail_in = row(b.d["tail"])
+    mtla.mtla_paged_append(b.md, b.B + 1, c, m, 10000.0, _behind(b.d["q_rope"], off), q, paged, tail_in, tail, t, n, state,
+                           None, 0, b.err)
+    b.check_append({"t": t[1:], "len": n[1:], "state": state[off:], "q": q[off:], "tail": tail[1:]})
+    del m, state, q
+
+    b.fill_groups()
+    off = (1 << 31) // (b.H * b.r) + 5
+    N, c = chunk(off)
+    out = _behind(torch.full((b.N, b.H, b.r), float("nan"), dtype=b.d["q_abs"].dtype, device="cuda"), off)
+    lse = _behind(torch.full((b.N, b.H), float("nan"), device="cuda"), off)
+    size = mtla.mtla_paged_workspace_bytes(b.md, b.B + 1, N, mtla.PAGED_ATTN)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    kind = mtla.MTLA_F32 if b.dtype == "f32" else mtla.MTLA_BF16
+    mtla.mtla_paged_attn(b.md, b.B + 1, c, _behind(b.d["q_abs"], off), _behind(b.d["q_rope"], off), _behind(b.d["state"], off),
+                         paged, out, kind, lse, ws, size, b.err)
+    b.check_attn({"out": out[off:], "lse": lse[off:]})
+    assert int(b.err.item()) == 0
+
+
 # ------------------------------------------------------------ verification
 
 
@@ -412,6 +489,27 @@ def test_verify_blocks(V, lens):
             ua, u = rng.random(N).astype(np.float32), us.astype(np.float32)
             keep, nxt, err = _verify(p, Q, tokens, start, ua, u)
             assert (keep, nxt) == verify_ref(p, Q, tokens, start, ua, u) and err == 0
+
+
+def test_verify_far_rows(freed):
+    """Rows 2^30 entries apart."""
+    rng = np.random.default_rng(3)
+    V, lens, ld = 1000, [2, 0, 2], 1 << 30
+    start = np.concatenate([[0], np.cumsum(lens)])
+    N = int(start[-1])
+    p, q = _dists(rng, N, V)
+    tokens = rng.integers(0, V, N)
+    dev = lambda v, dt: torch.tensor(np.asarray(v, dt), device="cuda")
+    far = [torch.empty(N, ld, device="cuda") for _ in range(2)]
+    for x, y in zip(far, (p, q)):
+        x[:, :V] = torch.from_numpy(y).cuda()
+    for accept in (0.0, 0.999):
+        ua, us = np.full(N, accept, np.float32), rng.random(len(lens)).astype(np.float32)
+        keep, nxt, err = dev([-9] * 3, np.int32), dev([-9] * 3, np.int32), dev([0], np.int32)
+        mtla.mtla_verify_drafts(3, N, V, far[0], ld, far[1], ld, dev(tokens, np.int32), dev(start, np.int32), dev(ua, np.float32),
+                                dev(us, np.float32), keep, nxt, err)
+        torch.cuda.synchronize()
+        assert (keep.tolist(), nxt.tolist()) == verify_ref(p, q, tokens, start, ua, us) and int(err.item()) == 0
 
 
 def test_verify_odd_distributions():
