@@ -498,6 +498,8 @@ mtla_status mtla_paged_append(const mtla_dims *dims, int32_t B, const mtla_chunk
  * It reads the cache as mtla_paged_append of the same chunk left it.  One token
  * a sequence is a decode step, several a speculative step, many a piece of a
  * prompt.
+ * NaN and infinite values reach the queries that see them and no others: what a
+ * later token of the chunk holds changes nothing for the earlier ones.
  *   q_abs [N, H, r], q_rope [N, H, d_R] (RoPE applied), row_state [N, D]: cache
  *   dtype; out [N, H, r] in out_dtype (the cache dtype, or MTLA_F32); lse
  *   [N, H] fp32 (nullable).

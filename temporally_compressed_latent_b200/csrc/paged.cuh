@@ -510,6 +510,55 @@ struct PagedAttnArgs {
   float scale_log2;  // log2(e) / sqrt(d_h)
 };
 
+// ----------------------------------------------------------------------------
+// NaN and infinite values of an item's keys.
+//
+// The rows of an M tile share every key tile, so the value product also takes
+// columns that some of its rows do not see (a later token's own state, a group
+// that a later token closed), with probability zero; 0 x NaN and 0 x inf would
+// hand a later token's values to an earlier one.  Such a column's score is itself
+// not finite, whatever the query.  So where a hidden score is not finite, the
+// column's latents that are not finite become zeros before the value product,
+// and the rows that do see the column get their NaN back when the item is stored
+// (p v is NaN for every such v that a row sees: its score is NaN or +inf, and with
+// it every p, or -inf, and p = 0).  Ordinary values pay for the look alone.
+// ----------------------------------------------------------------------------
+// the elements of a 32-bit word that are not finite, as zeros
+template <typename T> __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w);
+template <> __device__ __forceinline__ uint32_t finite_or_zero<float>(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u ? 0u : w; }
+template <> __device__ __forceinline__ uint32_t finite_or_zero<__nv_bfloat16>(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  return (w & 0x7f800000u) == 0x7f800000u ? w & 0xffffu : w;
+}
+// Rows [i0, i1) of an item's M tile (a multiple of r elements apart from dst, row
+// 0's; fp32 or T), by the warp that has stored them: NaN in every channel in which
+// a column that the row sees, and that not all rows of the item see, is not finite.
+template <typename T>
+static __device__ __noinline__ void restore_nan(const PagedAttnArgs& a, int b, int row0, int64_t t, int i0, int i1, void* dst,
+                                                bool f32) {
+  const int lane = threadIdx.x & 31;
+  const int64_t g0 = rows_below(a.plan, t);
+  __syncwarp();
+  for (int i = i0; i < i1; ++i) {
+    const int tok = i / a.H;
+    const int64_t g1 = rows_below(a.plan, t + tok);
+    for (int64_t g = g0; g <= g1; ++g) {
+      const T* src = reinterpret_cast<const T*>(a.row_state) + (int64_t)(row0 + tok) * (a.r + a.d_R);
+      if (g < g1) {
+        const int64_t row = pool_row(a.p, b, g);
+        if (row < 0) continue;
+        src = reinterpret_cast<const T*>(a.p.pages) + row * a.p.row_stride;
+      }
+      for (int e = lane; e < a.r; e += 32) {
+        if (isfinite(ld_f32(src + e))) continue;
+        const int64_t at = (int64_t)i * a.r + e;
+        if (f32) reinterpret_cast<float*>(dst)[at] = __int_as_float(0x7fc00000);
+        else st_elem(reinterpret_cast<T*>(dst) + at, __int_as_float(0x7fc00000));
+      }
+    }
+  }
+}
+
 // generic kernel (paged_attn.cu)
 constexpr int PSM = 32;  // M tile rows
 constexpr int PSN = 32;  // key tile rows

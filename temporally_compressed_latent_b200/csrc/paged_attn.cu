@@ -78,12 +78,25 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Zeros in the place of a key tile's latents that are not finite, in its virtual
+// rows from `from` on (those below are seen by every row of the item).  The
+// block's barrier after the softmax comes before the value product.
+template <typename T>
+static __device__ __noinline__ void hide_latents(uint8_t* tile, int pitch, int r, uint32_t v0, uint32_t from) {
+  const int words = r * (int)sizeof(T) / 4;
+  for (int k = threadIdx.x >> 5; k < PSN; k += NT / 32) {
+    if (v0 + k < from) continue;
+    uint32_t* const row = reinterpret_cast<uint32_t*>(tile + k * pitch);
+    for (int e = threadIdx.x & 31; e < words; e += 32) row[e] = finite_or_zero<T>(row[e]);
+  }
+}
+
 // NQ: channel quads per lane, ceil(r / 128); 0: r <= 64, where lanes 16 .. 31
 // take every second key.  Three blocks an SM where the running output is small
 // (8 sequences of up to 33 tokens over 500 rows, r = 64: 19.1 us; two blocks
 // 21.7, four, whose registers spill, 21.9).
 template <typename T, int NQ0>
-__global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_attn_simt_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_attn_simt_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int NQ = NQ0 > 0 ? NQ0 : 1, NK = NQ0 > 0 ? 1 : 2;  // channel quads; key groups of a warp
   const int kg = NK == 2 ? (int)(threadIdx.x & 31) >> 4 : 0, cl = NK == 2 ? (int)threadIdx.x & 15 : (int)threadIdx.x & 31;
   extern __shared__ float smem[];
@@ -99,6 +112,7 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
   ItemWalk* walks = reinterpret_cast<ItemWalk*>(wins + WINS);  // the first warp's, a lane each: no registers between items
   Item* sit = reinterpret_cast<Item*>(walks + 32);
   int* more = reinterpret_cast<int*>(sit + 1);
+  int* hid = more + 1;                    // a score that its row does not see is not finite (see restore_nan)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grid = gridDim.x, x = blockIdx.x;
 
@@ -118,6 +132,7 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
       walks[lane] = walk;
       if (lane == 0) {
         *more = any;
+        *hid = 0;
         if (any) *sit = it;
       }
       if (any && it.slot >= 0 && it.kt1 == it.kt && lane == 0)  // a split item ends here
@@ -227,13 +242,16 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
       const float s00 = both(t00), s01 = both(t01), s10 = both(t10), s11 = both(t11);
       auto put = [&](int k, int c, float v) {
         const uint32_t g = v0 + c;
-        Ss[c * (PSM + 4) + r0 + 16 * k] = g < seen[k] || g == own[k] ? v * a.scale_log2 : -INFINITY;
+        const bool sees = g < seen[k] || g == own[k];
+        Ss[c * (PSM + 4) + r0 + 16 * k] = sees ? v * a.scale_log2 : -INFINITY;
+        if (!sees && own[k] != 0xffffffffu && !isfinite(v) && (g < R || g - R8 < (uint32_t)it.ntok)) *hid = 1;
       };
       put(0, c0, s00);
       put(0, c0 + 16, s01);
       put(1, c0, s10);
       put(1, c0 + 16, s11);
       __syncthreads();
+      if (*hid) hide_latents<T>(Kb + ((kt - it.kt0) & 1) * PSN * KP, KP, a.r, v0, rows_below(a.plan, it.t));
       {  // softmax: eight lanes a row, four keys each
         const int i = tid >> 3, k0 = tid & 7;
         float xv[4], mx = -INFINITY;
@@ -327,6 +345,14 @@ __global__ void __launch_bounds__(NT, NQ0 < 2 ? 3 : (NQ0 == 2 ? 2 : 1)) paged_at
           }
         }
       }
+    }
+    if (*hid && 4 * warp < live) {
+      const bool f32 = it.slot >= 0 || a.out_f32 || sizeof(T) == 4;
+      const int64_t first = it.slot >= 0 ? (int64_t)it.slot * a.rows : (int64_t)it.row0 * a.H;
+      void* const dst = it.slot >= 0 ? (void*)(a.part.o + first * a.r)
+                                     : (f32 ? (void*)(reinterpret_cast<float*>(a.out) + first * a.r)
+                                            : (void*)(reinterpret_cast<T*>(a.out) + first * a.r));
+      restore_nan<T>(a, it.b, it.row0, it.t, 4 * warp, live < 4 * warp + 4 ? live : 4 * warp + 4, dst, f32);
     }
     __syncthreads();  // the item and its statistics have been read
   }

@@ -91,7 +91,8 @@ __host__ __device__ constexpr uint32_t keys_off(int stages) {
 static_assert(keys_off(4) + 4 * KBYTES <= OPERANDS && keys_off(3) + 3 * KBYTES <= OPERANDS, "stages");
 constexpr size_t OFF_OST = OPERANDS;
 constexpr size_t OFF_XCH = OFF_OST + (size_t)EPW * OST_BYTES;  // maxima [2][2][BM], sums [2][2][BM], final maxima [2][BM]
-constexpr size_t OFF_RING = OFF_XCH + 10 * BM * 4;
+constexpr size_t OFF_HID = OFF_XCH + 10 * BM * 4;              // [2] items: a byte a softmax warp that hid values
+constexpr size_t OFF_RING = OFF_HID + 2 * SMW;
 constexpr size_t OFF_WIN = OFF_RING + RING * sizeof(RingItem);
 constexpr size_t OFF_PLAN = OFF_WIN + WINS * sizeof(SeqWin);
 constexpr size_t OFF_BAR = (OFF_PLAN + sizeof(PlanShared) + 15) / 16 * 16;
@@ -132,6 +133,35 @@ __device__ __forceinline__ int tile_groups(int R8g, int ntok, int kt) {
   return left < BN / 8 ? left : BN / 8;
 }
 
+// Zeros in the place of the latents of a key tile's columns c0 + c (bit c of
+// `hidden`) that are not finite (a warp; see restore_nan).  The score MMA has read
+// the tile, the value MMA waits for this warp; another warp may do the same.
+static __device__ __noinline__ void hide_latents(uint8_t* stage, int c0, uint32_t hidden) {
+  const int lane = threadIdx.x & 31;
+  for (; hidden; hidden &= hidden - 1) {
+    const int r = c0 + __ffs(hidden) - 1;
+    uint4* const at = reinterpret_cast<uint4*>(stage + (r >> 3) * GRP + (lane >> 2) * 512 + (r & 7) * 64 + (lane & 3) * 16);
+    const uint4 v = *at;
+    *at = make_uint4(finite_or_zero<__nv_bfloat16>(v.x), finite_or_zero<__nv_bfloat16>(v.y),
+                     finite_or_zero<__nv_bfloat16>(v.z), finite_or_zero<__nv_bfloat16>(v.w));
+  }
+  fence_proxy_async_smem();
+}
+// one of 32 values is not finite: x 0 is NaN then (two a packed instruction)
+__device__ __forceinline__ bool not_finite(const float (&x)[32]) {
+  uint64_t z[2] = {0, 0}, v;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[c]), "f"(x[c + 1]));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(z[c >> 1 & 1]) : "l"(v), "l"(uint64_t(0)));
+  }
+  float a, b;
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(z[0]) : "l"(z[1]));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(z[0]));
+  return a + b != 0.f;
+}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
 __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_constant__ PagedAttnMaps mp,
                                                               const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -158,6 +188,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   float* xmax = reinterpret_cast<float*>(sm + OFF_XCH);   // [2 tile parity][2 halves][BM]
   float* xl = xmax + 4 * BM;                              // [2 item parity][2 halves][BM]
   float* xm = xl + 4 * BM;                                // [2 item parity][BM]
+  uint8_t* const hid = sm + OFF_HID;                      // [2 item parity][SMW]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -393,6 +424,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       if (ok && !warp_wait(&stat_full[sb2], (n >> 1) & 1)) ok = false;
       const float m = xm[sb2 * BM + i];
       const float l = xl[(sb2 * 2 + 0) * BM + i] + xl[(sb2 * 2 + 1) * BM + i];
+      const bool hidden = *reinterpret_cast<const uint64_t*>(hid + sb2 * SMW) != 0;  // values of columns that some row does not see
       __syncwarp();
       if (lane == 0) mbar_arrive(&stat_empty[sb2]);
       const bool part = it.slot >= 0;
@@ -431,6 +463,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
                               __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
           }
         }
+        if (hidden)
+          restore_nan<__nv_bfloat16>(a, it.b, it.row0, it.t, qe * 32, live < qe * 32 + 32 ? live : qe * 32 + 32,
+                                     dst - (int64_t)i * R, true);
         continue;
       }
       __nv_bfloat16* const base = static_cast<__nv_bfloat16*>(a.out) + (row - lane) * R;  // the quarter's first row
@@ -467,6 +502,9 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           }
         }
       }
+      if (hidden)
+        restore_nan<__nv_bfloat16>(a, it.b, it.row0, it.t, qe * 32, live < qe * 32 + 32 ? live : qe * 32 + 32,
+                                   base - (int64_t)qe * 32 * R, false);
     }
     if (!ok && lane == 0) set_err(a.dev_err, MTLA_DEVERR_TIMEOUT);
   } else {
@@ -493,6 +531,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       const int seen = on ? rows_below(a.plan, it.t + tok) : 0x7fffffff;
       const int own = on ? R8 + tok : -1;
       float m_run = -INFINITY, l = 0.f;  // l: this half's sum
+      bool hides = false;                // this warp has hidden values of the item
       for (int kt = it.kt0; kt < it.kt1; ++kt, ++kc) {
         const int sb = kc % NSB, xb = kc & 1;
         if (ok && !warp_wait(&s_full[sb], (kc / NSB) & 1)) ok = false;
@@ -518,9 +557,24 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           const int c0 = kt * BN + 32 * hf, nvis = seen - c0;
           if (!__all_sync(0xffffffffu, nvis >= 32)) {  // some row does not see all of these columns
             const int self = own - c0;
+            const uint32_t vis = low_bits(nvis) | ((uint32_t)self < 32u ? 1u << self : 0u);
+            // columns of the item that this row does not see
+            const uint32_t not_mine =
+                on ? (low_bits(it.R - c0) | (low_bits(R8 + it.ntok - c0) & ~low_bits(R8 - c0))) & ~vis : 0u;
+            if (__any_sync(0xffffffffu, not_mine != 0u) && __any_sync(0xffffffffu, not_finite(x))) {
+              // some score is not finite: of a column that its row does not see?
+              float z = 0.f;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (not_mine >> c & 1) z = fmaf(x[c], 0.f, z);
+              if (__any_sync(0xffffffffu, z != 0.f)) {
+                hide_latents(sm + stage_off(st), 32 * hf, __reduce_or_sync(0xffffffffu, not_mine));
+                hides = true;
+              }
+            }
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (!(c < nvis || c == self)) x[c] = -INFINITY;
+              if (!(vis >> c & 1)) x[c] = -INFINITY;
           }
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four independent chains
 #pragma unroll
@@ -581,6 +635,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       if (ok && n >= 2 && !warp_wait(&stat_empty[sb2], ((n >> 1) & 1) ^ 1)) ok = false;
       xl[(sb2 * 2 + hf) * BM + i] = l;
       if (hf == 0) xm[sb2 * BM + i] = m_run;
+      if (lane == 0) hid[sb2 * SMW + warp] = hides;
       __syncwarp();
       if (lane == 0) mbar_arrive(&stat_full[sb2]);
     }
