@@ -499,7 +499,9 @@ mtla_status mtla_paged_append(const mtla_dims *dims, int32_t B, const mtla_chunk
  * a sequence is a decode step, several a speculative step, many a piece of a
  * prompt.
  * NaN and infinite values reach the queries that see them and no others: what a
- * later token of the chunk holds changes nothing for the earlier ones.
+ * later token of the chunk holds changes nothing for the earlier ones.  A query
+ * with a score that is NaN or +inf has NaN outputs and a NaN lse; a column that
+ * scores -inf has probability zero, and makes the output NaN where it is infinite.
  *   q_abs [N, H, r], q_rope [N, H, d_R] (RoPE applied), row_state [N, D]: cache
  *   dtype; out [N, H, r] in out_dtype (the cache dtype, or MTLA_F32); lse
  *   [N, H] fp32 (nullable).

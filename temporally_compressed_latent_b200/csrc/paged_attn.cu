@@ -453,9 +453,9 @@ __global__ void __launch_bounds__(CNT, 8) paged_combine_kernel(const __grid_cons
         }
 #pragma unroll
         for (int u = 0; u < CNP; ++u) {
-          // (a part with nothing visible to this row holds no values of it)
+          // (a part with nothing visible to this row has m = -inf and zeros; one
+          // whose only visible scores are NaN has m = -inf too, and its NaN stays)
           const float w = exp2f(ml[u].x - ref);
-          if (!(w > 0.f)) continue;
           L = fmaf(ml[u].y, w, L);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

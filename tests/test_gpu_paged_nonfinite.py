@@ -118,3 +118,29 @@ def test_later_values_do_not_reach_earlier_tokens(new, past, dims, value):
         if new is SHORT[0]:
             check(b, o)
     assert int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("dims", [{}, dict(H=16), TINY, WIDE], ids=["main", "h16", "tiny", "wide"])
+@pytest.mark.parametrize("new,past", [([1] * 32, [4096] * 32), ([1] * 32, [21] * 32), LONG], ids=["split", "whole", "long"])
+def test_seen_values_reach_the_output(new, past, dims, value):
+    """A token's own state (in a cut item it can be a part's only visible column), an old cache row, a query; with a
+    query that is zero where the state is not finite."""
+    b = Batch(new, past, s=2, page_rows=8, seed=52, **dims)
+    b.fill_groups()
+    for seq, n in enumerate(new):
+        if seq % 4 < 3 or n > 1:
+            put_state(b, seq, n - 1, 5, value)
+        if seq % 4 == 1:
+            put_row(b, seq, past[seq] // 4, b.r - 1, value)
+        if seq % 4 == 2:
+            tok = int(b.start[seq]) + n - 1
+            b.d["q_abs"][tok, 0, 5] = 0.0
+            b.v["q_abs"][tok, 0, 5] = 0.0
+        if seq % 4 == 3:
+            tok = int(b.start[seq]) + n // 2
+            b.d["q_abs"][tok, :, 2] = value
+            b.v["q_abs"][tok, :, 2] = value
+    for od in ("f32", b.dtype):
+        check(b, b.attn(out_dtype=od))
+    assert int(b.err.item()) == 0
