@@ -505,8 +505,11 @@ mtla_status mtla_paged_append(const mtla_dims *dims, int32_t B, const mtla_chunk
  *   q_abs [N, H, r], q_rope [N, H, d_R] (RoPE applied), row_state [N, D]: cache
  *   dtype; out [N, H, r] in out_dtype (the cache dtype, or MTLA_F32); lse
  *   [N, H] fp32 (nullable).
- * A sequence whose rows exceed its table (or times leave [0, 2^31)) sets
- * MTLA_DEVERR_CAPACITY and its rows of out and lse are left as they were.
+ * A sequence whose rows exceed its table (ceil((t_prev + tokens)/s) above
+ * table_pages * page_rows, as in the append; or times leave [0, 2^31)) sets
+ * MTLA_DEVERR_CAPACITY and its rows of out and lse are left as they were.  This
+ * call does not know J_max: the chunk of a sequence that the append refused with
+ * MTLA_DEVERR_PE_RANGE has no row states and is not to be attended.
  *   workspace: mtla_paged_workspace_bytes(dims, B, N, MTLA_PAGED_ATTN) bytes; no
  *   initialisation; for calls that run one after another.
  */

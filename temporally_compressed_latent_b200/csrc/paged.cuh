@@ -293,11 +293,12 @@ struct PlanShared {
 };
 
 // The chunk window the attention takes (a sequence whose rows exceed its table,
-// or whose times leave [0, 2^31), takes none).
+// or whose times leave [0, 2^31), takes none: those that the append refuses for
+// want of room have no states to attend).
 __device__ __forceinline__ SeqWin attn_win(const ChunkDev& c, const PagesDev& p, const FastDiv& div_s, int b,
                                            int32_t* dev_err) {
   SeqWin w = seq_win(c, b);
-  if (w.n > 0 && (w.t0 < 0 || w.t0 + w.n > 0x7fffffff || (int64_t)div32((uint32_t)(w.t0 + w.n - 1), div_s) > table_rows(p))) {
+  if (w.n > 0 && (w.t0 < 0 || w.t0 + w.n > 0x7fffffff || (int64_t)div32((uint32_t)(w.t0 + w.n - 1), div_s) >= table_rows(p))) {
     if (dev_err) set_err(dev_err, MTLA_DEVERR_CAPACITY);
     w.n = 0;
   }
