@@ -65,7 +65,9 @@ __device__ __forceinline__ int64_t pool_row(const PagesDev& p, int b, int64_t g)
   return page >= 0 && page < p.num_pages ? (int64_t)page * p.page_rows + (g - k * p.page_rows) : -1;
 }
 
-// The sequence that owns token row i: the last b with tok_start[b] <= i, or -1.
+// The sequence that owns token row i: the last b with tok_start[b] <= i, or -1
+// (of starts that do not ascend any b, whose window need not hold i: the callers
+// look at both of its ends).
 // Taken by a whole warp: every round narrows the range 32-fold (two dependent
 // loads for 1024 sequences; a binary search by one thread would take ten).
 __device__ __forceinline__ int warp_find_seq(const int32_t* tok_start, int B, int i) {

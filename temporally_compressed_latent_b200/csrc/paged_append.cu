@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
     w.first = __shfl_sync(0xffffffffu, w.first, 0);
     w.n = __shfl_sync(0xffffffffu, w.n, 0);
     w.t0 = __shfl_sync(0xffffffffu, w.t0, 0);
-    if (b < 0 || i - w.first >= w.n) return;
+    if (b < 0 || i < w.first || i - w.first >= w.n) return;
     const uint32_t pos = (uint32_t)(w.t0 + (i - w.first));
     const T* src = reinterpret_cast<const T*>(a.q_rope) + (int64_t)i * a.H * a.d_R;
     T* dst = reinterpret_cast<T*>(a.q_rope_out) + (int64_t)i * a.H * a.d_R;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
       if (lane == 0) {
         const int64_t place = i_beg - w.first;
         int64_t back = 0;
-        if (b >= 0 && place < w.n) {
+        if (b >= 0 && place >= 0 && place < w.n) {
           const uint32_t t = (uint32_t)(w.t0 + place), in = t - div32(t, a.div_s) * (uint32_t)s;
           back = in < place ? (int64_t)in : place;
         }
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
       t.seq = -1;
       t.group = t.pos = 0;
       t.opens = t.carry = t.last = t.row = 0;
-      if (lane < nu && i >= 0 && b >= 0 && place < w.n) {
+      if (lane < nu && i >= 0 && b >= 0 && place >= 0 && place < w.n) {
         t.seq = b;
         t.pos = (uint32_t)(w.t0 + place);
         t.group = div32(t.pos, a.div_s);

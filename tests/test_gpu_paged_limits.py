@@ -26,3 +26,36 @@ def test_append_and_attention_refuse_the_same_sequences(n, dims):
         b.take = [n, n, 0]
         getattr(b, "check_" + call)(o)
         assert int(b.err.item()) == mtla.DEVERR_CAPACITY
+
+
+@pytest.mark.parametrize("dims,N", [({}, 64), (TINY, 64), (dict(TINY, s=12), 64), ({}, 600)], ids=["main", "tiny", "far", "many"])
+def test_starts_that_do_not_ascend(dims, N):
+    """Whatever tok_start holds, no call looks outside its arrays: a token that a search leads to the wrong sequence
+    is nobody's, and times follow the windows."""
+    rng = np.random.default_rng(N)
+    B = 100
+    for trial in range(6):
+        b = Batch([1] * (B - 1) + [N - B + 1] if N > B else [1] * N + [0] * (B - N), [9] * B, page_rows=8,
+                  seed=43, J_extra=N, **{"s": 2, **dims})
+        b.fill_groups()
+        start = rng.integers(-5, N + 6, B + 1) if trial else np.arange(B, -1, -1)
+        b.tok_start.copy_(torch.from_numpy(start.astype(np.int32)))
+        b.table[:] = 0                                   # rows for any window: page 0 again and again
+        table = torch.zeros(B, 80, dtype=torch.int32, device="cuda")
+        b.paged = mtla.paged_cache(b.d_pages, b.num_pages, b.pr, b.stride, table, 80)
+        o = b.append()
+        a = b.attn()
+        first = np.clip(start[:-1], 0, N)
+        n = np.clip(np.minimum(start[1:], N) - first, 0, None)
+        torch.cuda.synchronize()
+        assert o["t"].tolist() == (9 + n).tolist() and int(b.err.item()) == 0
+        seen = np.zeros(N, bool)
+        for f, k in zip(first, n):
+            seen[f:f + k] = True
+        assert torch.isnan(a["out"][torch.from_numpy(~seen).cuda()]).all()
+        keep, nxt = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        p = torch.rand(N, 50, device="cuda")
+        mtla.mtla_verify_drafts(B, N, 50, p, 50, None, 0, torch.zeros(N, dtype=torch.int32, device="cuda"), b.tok_start,
+                                torch.zeros(N, device="cuda"), torch.full((B,), 0.5, device="cuda"), keep, nxt, b.err)
+        torch.cuda.synchronize()
+        assert ((keep.cpu().numpy() == 0) == (n == 0)).all() and int(b.err.item()) == 0
