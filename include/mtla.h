@@ -464,14 +464,16 @@ typedef struct {
  *             ceil(t_out / s).
  *   merge: c_new [N, r], kR_new [N, d_R] (cache dtype); W_c, b_c, P, J_max.
  *   q_rope    [N, H, d_R] (nullable): the chunk's RoPE queries, written rotated
- *             (at the token's position, cache dtype) to q_rope_out, which may
- *             be q_rope itself.
- * Only t_out, tail_out, row_state, q_rope_out and cache rows are written, and
- * no state that is read is overwritten: tail_out and t_out must not overlap
- * tail_in and t_prev.  So a chunk can be appended again with another tok_count:
- * after a verification, the call with tok_count = n_keep leaves the cache rows,
- * the tail and the lengths that the kept tokens alone would have left (rows of
- * later groups hold stale values until they are appended again).  How a
+ *             (at the token's position, cache dtype) to q_rope_out, which is
+ *             q_rope itself or does not overlap it.
+ * Only t_out, cache_len, tail_out, row_state, q_rope_out and cache rows are
+ * written, and no state that is read is overwritten: tail_out and t_out must not
+ * overlap tail_in and t_prev.  So a chunk can be appended again with another
+ * tok_count: after a verification, the call with tok_count = n_keep leaves the
+ * cache rows, the tail and the lengths that the kept tokens alone would have left
+ * (rows of later groups hold stale values until they are appended again).  Queries
+ * rotated in place are rotated already: the repeated call takes q_rope =
+ * q_rope_out = NULL then.  How a
  * sequence's tokens are cut into chunks does not change the sums: the open
  * group's sum travels in fp32.
  * A sequence whose chunk does not fit (ceil((t_prev + tokens)/s) above

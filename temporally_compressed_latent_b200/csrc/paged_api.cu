@@ -151,6 +151,9 @@ mtla_status mtla_paged_append(const mtla_dims* dims, int32_t B, const mtla_chunk
       (cache_len && overlap(chunk->t_prev, (size_t)B * 4, cache_len, (size_t)B * 4)))
     return MTLA_ERR_INVALID_ARG;
   if ((int64_t)chunk->N * dims->H >= (int64_t(1) << 31)) return MTLA_ERR_UNSUPPORTED;
+  // queries are rotated in place or into an array of their own
+  const size_t q_bytes = (size_t)chunk->N * dims->H * dims->d_R * elem(dims->dtype);
+  if (q_rope && q_rope_out && q_rope != q_rope_out && overlap(q_rope, q_bytes, q_rope_out, q_bytes)) return MTLA_ERR_INVALID_ARG;
   if (B == 0) return MTLA_OK;
   a.m.c_new = merge->c_new;
   a.m.kR_new = merge->kR_new;

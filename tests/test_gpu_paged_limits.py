@@ -59,3 +59,27 @@ def test_starts_that_do_not_ascend(dims, N):
                                 torch.zeros(N, device="cuda"), torch.full((B,), 0.5, device="cuda"), keep, nxt, b.err)
         torch.cuda.synchronize()
         assert ((keep.cpu().numpy() == 0) == (n == 0)).all() and int(b.err.item()) == 0
+
+
+@pytest.mark.parametrize("dims,new", [({}, [7, 3]), (TINY, [7, 3]), ({}, [600, 3])], ids=["main", "tiny", "many"])
+def test_taken_back_after_queries_in_place(dims, new):
+    """The first call rotates the queries where they are; the repeated one takes none, and they stay rotated once."""
+    b = Batch(new, [4, 9], s=2, page_rows=8, seed=44, **dims)
+    first = b.append(in_place=True)
+    torch.cuda.synchronize()
+    once = first["q"].clone()
+    keep = torch.tensor([2, 3], dtype=torch.int32, device="cuda")
+    back = b.append(q=False, chunk=mtla.chunk(b.N, b.tok_start, b.t_prev, keep))
+    torch.cuda.synchronize()
+    assert torch.equal(first["q"], once)
+    few = Batch(new, [4, 9], s=2, page_rows=8, seed=44, count=[2, 3], **dims)
+    few.check_append(few.append())
+    alone = few.append(q=False)
+    torch.cuda.synchronize()
+    assert torch.equal(back["tail"], alone["tail"]) and torch.equal(back["t"], alone["t"])
+    Q = b.append_ref()[-1]
+    q = first["q"].double().cpu().numpy()
+    for i, ref in Q.items():
+        gap = 2.0 ** -20 * np.abs(b.v["q_rope"][i]).max()
+        half = 2.0 ** -8 if b.dtype == "bf16" else 2.0 ** -24
+        np.testing.assert_array_less(np.abs(q[i] - ref), gap + half * (np.abs(ref) + gap) + 1e-30)
