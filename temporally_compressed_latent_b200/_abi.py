@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import sys
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmtla.so")
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mtla.h")
@@ -38,16 +39,19 @@ class _Dims(_c.Structure):
 
 
 class _Merge(_c.Structure):
+    _devs = ()  # devices of the tensors behind the addresses
     _fields_ = [("c_new", _c.c_void_p), ("kR_new", _c.c_void_p), ("W_c", _c.c_void_p), ("b_c", _c.c_void_p),
                 ("P", _c.c_void_p), ("J_max", _c.c_int32)]
 
 
 class _Paged(_c.Structure):
+    _devs = ()
     _fields_ = [("pages", _c.c_void_p), ("num_pages", _c.c_int64), ("row_stride", _c.c_int64),
                 ("page_rows", _c.c_int32), ("table_pages", _c.c_int32), ("block_table", _c.c_void_p)]
 
 
 class _Chunk(_c.Structure):
+    _devs = ()
     _fields_ = [("N", _c.c_int32), ("reserved", _c.c_int32), ("tok_start", _c.c_void_p), ("tok_count", _c.c_void_p),
                 ("t_prev", _c.c_void_p)]
 
@@ -164,10 +168,16 @@ def _merge(m):
     return _c.byref(st)
 
 
+def _devices(*tensors):
+    """The devices that these tensors are on, -1 the host (addresses, None and pinned host memory have none)."""
+    return tuple({x.get_device() for x in tensors if hasattr(x, "get_device") and not (x.get_device() < 0 and x.is_pinned())})
+
+
 def merge_args(c_new, kR_new, W_c, b_c, P, J_max) -> _Merge:
     """mtla_merge_args of these tensors, for the paged calls; keeps them alive."""
     m = _Merge(_ptr(c_new), _ptr(kR_new), _ptr(W_c), _ptr(b_c), _ptr(P), J_max)
     m._keep = (c_new, kR_new, W_c, b_c, P)
+    m._devs = _devices(c_new, kR_new, W_c, b_c, P)
     return m
 
 
@@ -175,6 +185,7 @@ def chunk(N, tok_start, t_prev, tok_count=None) -> _Chunk:
     """mtla_chunk: the new tokens of a batch; keeps its tensors alive."""
     c = _Chunk(N, 0, _ptr(tok_start), _ptr(tok_count), _ptr(t_prev))
     c._keep = (tok_start, tok_count, t_prev)
+    c._devs = _devices(tok_start, tok_count, t_prev)
     return c
 
 
@@ -182,6 +193,7 @@ def paged_cache(pages, num_pages, page_rows, row_stride, block_table, table_page
     """mtla_paged_cache: a pool of pages and the sequences' block tables; keeps its tensors alive."""
     c = _Paged(_ptr(pages), num_pages, row_stride, page_rows, table_pages, _ptr(block_table))
     c._keep = (pages, block_table)
+    c._devs = _devices(pages, block_table)
     return c
 
 
@@ -292,38 +304,65 @@ def mtla_paged_workspace_bytes(d, B, N, which) -> int:
     return int(lib.mtla_paged_workspace_bytes(_c.byref(d), B, N, which))
 
 
-def _paged_stream(stream, dev_err):
-    """The stream of a paged call.  Launches go to the current device: tensors of another one are refused
-    (a stream given by the caller is taken as it is)."""
-    if stream is not None or isinstance(dev_err, int):
-        return _stream(stream)
+def _paged_args(stream, structs, tensors):
+    """The addresses of a paged call's tensors, and its stream.  Kernels are launched on the current device: a
+    tensor that is somewhere else (one behind the argument structs too) is refused, but for pinned host memory;
+    addresses are taken as they are."""
+    dev, out = None, []
+    for x in tensors:
+        if x is None:
+            out.append(None)
+            continue
+        try:
+            d = x.get_device()
+        except AttributeError:  # an address
+            out.append(x)
+            continue
+        if d != dev and not (d < 0 and x.is_pinned()):
+            dev = _current_device(d)
+        out.append(x.data_ptr())
+    for st in structs:
+        for d in st._devs:
+            if d != dev:
+                dev = _current_device(d)
+    if stream is None and dev is not None:
+        out.append(sys.modules["torch"]._C._cuda_getCurrentRawStream(dev))  # the handle without building a stream object
+    else:
+        out.append(_stream(stream))
+    return out
+
+
+def _current_device(d):
     import torch
-    dev = torch.cuda.current_device()
-    if dev_err.get_device() != dev:
-        raise ValueError(f"the call's tensors are on {dev_err.device}, the current device is cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev)  # the handle without building a stream object
+    at = torch.cuda.current_device()
+    if d != at:
+        raise ValueError(f"a tensor of the call is on {'the host' if d < 0 else f'cuda:{d}'}, the current device is cuda:{at}")
+    return at
 
 
 def mtla_paged_append(d, B, chunk, merge, rope_base, q_rope, q_rope_out, cache, tail_in, tail_out, t_out, cache_len,
                       row_state, workspace, workspace_bytes, dev_err, stream=None):
-    _check(lib.mtla_paged_append(_c.byref(d), B, _c.byref(chunk), _c.byref(merge), rope_base, _ptr(q_rope),
-                                 _ptr(q_rope_out), _c.byref(cache), _ptr(tail_in), _ptr(tail_out), _ptr(t_out),
-                                 _ptr(cache_len), _ptr(row_state), _ptr(workspace), workspace_bytes, _ptr(dev_err),
-                                 _paged_stream(stream, dev_err)), "mtla_paged_append")
+    q, qo, ti, to, t, n, rows, ws, err, st = _paged_args(
+        stream, (chunk, merge, cache),
+        (q_rope, q_rope_out, tail_in, tail_out, t_out, cache_len, row_state, workspace, dev_err))
+    _check(lib.mtla_paged_append(d, B, chunk, merge, rope_base, q, qo, cache, ti, to, t, n, rows, ws, workspace_bytes,
+                                 err, st), "mtla_paged_append")
 
 
 def mtla_paged_attn(d, B, chunk, q_abs, q_rope, row_state, cache, out, out_dtype, lse, workspace, workspace_bytes,
                     dev_err, stream=None):
-    _check(lib.mtla_paged_attn(_c.byref(d), B, _c.byref(chunk), _ptr(q_abs), _ptr(q_rope), _ptr(row_state),
-                               _c.byref(cache), _ptr(out), out_dtype, _ptr(lse), _ptr(workspace), workspace_bytes,
-                               _ptr(dev_err), _paged_stream(stream, dev_err)), "mtla_paged_attn")
+    qa, qr, rows, o, l, ws, err, st = _paged_args(stream, (chunk, cache),
+                                                  (q_abs, q_rope, row_state, out, lse, workspace, dev_err))
+    _check(lib.mtla_paged_attn(d, B, chunk, qa, qr, rows, cache, o, out_dtype, l, ws, workspace_bytes, err, st),
+           "mtla_paged_attn")
 
 
 def mtla_verify_drafts(B, N, V, p, ld_p, q, ld_q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err,
                        stream=None):
-    _check(lib.mtla_verify_drafts(B, N, V, _ptr(p), ld_p, _ptr(q), ld_q, _ptr(tokens), _ptr(tok_start),
-                                  _ptr(u_accept), _ptr(u_sample), _ptr(n_keep), _ptr(next_token), _ptr(dev_err),
-                                  _paged_stream(stream, dev_err)), "mtla_verify_drafts")
+    pp, qp, tok, start, ua, us, keep, nxt, err, st = _paged_args(
+        stream, (), (p, q, tokens, tok_start, u_accept, u_sample, n_keep, next_token, dev_err))
+    _check(lib.mtla_verify_drafts(B, N, V, pp, ld_p, qp, ld_q, tok, start, ua, us, keep, nxt, err, st),
+           "mtla_verify_drafts")
 
 
 def mtla_workspace_bytes(d, B, which=WS_DECODE) -> int:

@@ -83,3 +83,27 @@ def test_taken_back_after_queries_in_place(dims, new):
         gap = 2.0 ** -20 * np.abs(b.v["q_rope"][i]).max()
         half = 2.0 ** -8 if b.dtype == "bf16" else 2.0 ** -24
         np.testing.assert_array_less(np.abs(q[i] - ref), gap + half * (np.abs(ref) + gap) + 1e-30)
+
+
+def test_host_tensors_are_refused():
+    """Before anything is launched; pinned host memory is the device's too."""
+    b = Batch([2, 1], [4, 9], s=2, page_rows=8, seed=45)
+    for k in ("c", "q_rope", "tail"):
+        keep, b.d[k] = b.d[k], b.d[k].cpu()
+        with pytest.raises(ValueError, match="the host"):
+            b.append()
+        b.d[k] = keep
+    for k in ("q_abs", "state"):
+        keep, b.d[k] = b.d[k], b.d[k].cpu()
+        with pytest.raises(ValueError, match="the host"):
+            b.attn()
+        b.d[k] = keep
+    b.check_append(b.append())
+    p = torch.rand(3, 50, device="cuda")
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pin = lambda n: torch.full((n,), -9, dtype=torch.int32).pin_memory()
+    keep, nxt, err = pin(1), pin(1), torch.zeros(1, dtype=torch.int32).pin_memory()
+    u = torch.zeros(3, device="cuda")
+    mtla.mtla_verify_drafts(1, 3, 50, p, 50, p, 50, dev([0, 1, 77]), dev([0, 3]), u, u[:1], keep, nxt, err)
+    torch.cuda.synchronize()
+    assert keep.item() == 2 and 0 <= nxt.item() < 50 and err.item() == mtla.DEVERR_TOKEN
