@@ -473,9 +473,14 @@ typedef struct {
  * cache rows, the tail and the lengths that the kept tokens alone would have left
  * (rows of later groups hold stale values until they are appended again).  Queries
  * rotated in place are rotated already: the repeated call takes q_rope =
- * q_rope_out = NULL then.  How a
- * sequence's tokens are cut into chunks does not change the sums: the open
- * group's sum travels in fp32.
+ * q_rope_out = NULL then.
+ * The open group's sum travels in fp32, and sums run in token order from the
+ * group's start, so cutting a sequence's tokens into other chunks changes no more
+ * than roundings: with token arrays of fewer than 512 rows, or of other widths
+ * than bf16, r = 256, d_R = 32, s <= 64, nothing; above, the RoPE channels within
+ * 2^-19 of the key (their angles are exact every 8 tokens only).  Between the two,
+ * which multiply by W_c in fp32 and by two bf16 parts of it, a gate's
+ * pre-activation moves within 2^-15 of its terms' sizes.
  * A sequence whose chunk does not fit (ceil((t_prev + tokens)/s) above
  * table_pages * page_rows: MTLA_DEVERR_CAPACITY, as for times outside [0, 2^31);
  * above J_max: MTLA_DEVERR_PE_RANGE) takes none of its tokens.

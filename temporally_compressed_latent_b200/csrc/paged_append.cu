@@ -14,7 +14,7 @@
 // A tile that begins inside a group recomputes the entries of the group's
 // earlier tokens (at most s - 1), so that no block waits for another; the sums
 // run from the group's start in token order in every tile, which makes them
-// independent of the tiling.
+// independent of the tiling: one call or several give the same bits.
 //
 // Few tokens: the chain of dependent reads bounds it.  So W_c, the latents of
 // the first round (with a short stride the rows before a tile are taken
@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const __grid_constant_
           const float2 r = rope_cos_sin(t.pos, a.rope.turns[k >> 1]);
           x = (k & 1) ? yv[h] * r.y + x * r.x : x * r.x - yv[h] * r.y;
         }
-        e = tv[h] + x * sigmoidf_(g * pv[h]);
+        // (product and sum rounded one by one: the tail added here and the running
+        // sum added below give the same bits)
+        e = __fadd_rn(tv[h], __fmul_rn(x, sigmoidf_(g * pv[h])));
       }
       sm.v[u][lane] = e;
     }

@@ -107,3 +107,86 @@ def test_host_tensors_are_refused():
     mtla.mtla_verify_drafts(1, 3, 50, p, 50, p, 50, dev([0, 1, 77]), dev([0, 3]), u, u[:1], keep, nxt, err)
     torch.cuda.synchronize()
     assert keep.item() == 2 and 0 <= nxt.item() < 50 and err.item() == mtla.DEVERR_TOKEN
+
+
+def _in_pieces(b, cuts):
+    """The tokens of a one-sequence batch in pieces; tail, time and states as append() gives them."""
+    m = mtla.merge_args(b.d["c"], b.d["kR"], b.d["W_c"], b.d["b_c"], b.d["P"], b.d["P"].shape[0])
+    tail, t = b.d["tail"].clone(), b.t_prev.clone()
+    state, q = torch.full_like(b.d["state"], float("nan")), torch.full_like(b.d["q_rope"], float("nan"))
+    n = torch.zeros_like(t)
+    for lo, hi in zip(cuts[:-1], cuts[1:]):
+        start = torch.tensor([lo, hi], dtype=torch.int32, device="cuda")
+        tail2, t2 = torch.empty_like(tail), torch.empty_like(t)
+        mtla.mtla_paged_append(b.md, 1, mtla.chunk(b.N, start, t), m, BASE, b.d["q_rope"], q, b.paged, tail, tail2, t2, n,
+                               state, None, 0, b.err)
+        tail, t = tail2, t2
+    torch.cuda.synchronize()
+    return {"state": state, "tail": tail, "t": t, "len": n, "q": q}
+
+
+@pytest.mark.parametrize("dims,N,s,past", [
+    ({}, 40, 4, 6), ({}, 300, 2, 5), ({}, 1300, 2, 5), ({}, 900, 1, 0), ({}, 1000, 3, 1), ({}, 700, 9, 13), ({}, 1500, 64, 50),
+    (TINY, 200, 3, 4), (dict(TINY, r=128), 150, 30, 11), (dict(H=5, r=384, d_R=64), 90, 5, 2),
+])
+def test_pieces_give_the_bits_of_the_whole(dims, N, s, past):
+    """Within a kernel (chosen by the widths and the rows of the token arrays) a token's sums do not depend on the
+    call it comes in: the same bits, but for the RoPE channels of the tensor-core kernel, whose angles are exact at
+    every eighth column of a tile."""
+    make = lambda: Batch([N], [past], s=s, page_rows=16, seed=46, **dims)
+    whole = make()
+    ow = whole.append()
+    whole.check_append(ow)
+    same = whole.r if not dims and N >= 512 else whole.D           # channels whose bits do not change
+    # a rotated key is within 2^-20 of its size on either side, a group holds s of them, and each sum is rounded
+    size = whole.d["kR"].float().abs().max().item() if whole.d_R else 0.0
+    gap = s * (2 * 2.0 ** -20 * size + 2 * 2.0 ** -24 * s * size)
+    half = 2.0 ** -8 if whole.dtype == "bf16" else 0.0             # stored rows: a rounding each
+
+    def equal(x, y, stored, what):
+        x, y = x.float(), y.float()
+        assert torch.equal(x[..., :same], y[..., :same]), what
+        far = (x[..., same:] - y[..., same:]).abs() - gap - (half if stored else 0.0) * (x[..., same:].abs() + y[..., same:].abs())
+        assert same == whole.D or far.max().item() <= 0, what
+
+    rng = np.random.default_rng(N + s)
+    for trial in range(3):
+        most = (5, 60, 400)[trial]
+        cuts = [0]
+        while cuts[-1] < N:
+            cuts.append(min(N, cuts[-1] + int(rng.integers(1, most + 1))))
+        b = make()
+        o = _in_pieces(b, cuts)
+        for k in ("t", "len", "q"):
+            assert torch.equal(o[k], ow[k]), (k, trial)
+        equal(o["state"], ow["state"], True, ("state", trial))
+        equal(o["tail"], ow["tail"], False, ("tail", trial))
+        for j in range(past // s, -(-(past + N) // s)):
+            at = b.where(0, j)
+            equal(b.d_pages[at][: b.D], whole.d_pages[at][: b.D], True, ("row", j, trial))
+
+
+@pytest.mark.parametrize("s,past", [(2, 5), (7, 3), (64, 1)])
+def test_pieces_across_the_kernels(s, past):
+    """Token arrays of fewer than 512 rows take the kernel with the weights in fp32, longer ones that with two bf16
+    parts: a sequence may pass from one to the other and keeps the bounds of the latter."""
+    N = 1024
+    whole = Batch([N], [past], s=s, page_rows=16, seed=47)
+    b = Batch([N], [past], s=s, page_rows=16, seed=47)
+    tail, t = b.d["tail"].clone(), b.t_prev.clone()
+    state, q = torch.full_like(b.d["state"], float("nan")), torch.full_like(b.d["q_rope"], float("nan"))
+    n = torch.zeros_like(t)
+    for lo, hi in ((0, 130), (130, 700), (700, 701), (701, N)):
+        k = hi - lo
+        rows = lambda x: x[lo:hi].clone()
+        m = mtla.merge_args(rows(b.d["c"]), rows(b.d["kR"]), b.d["W_c"], b.d["b_c"], b.d["P"], b.d["P"].shape[0])
+        part, qp = torch.empty_like(state[lo:hi]), torch.empty_like(q[lo:hi])
+        start = torch.tensor([0, k], dtype=torch.int32, device="cuda")
+        tail2, t2 = torch.empty_like(tail), torch.empty_like(t)
+        mtla.mtla_paged_append(b.md, 1, mtla.chunk(k, start, t), m, BASE, rows(b.d["q_rope"]), qp, b.paged, tail, tail2, t2,
+                               n, part, None, 0, b.err)
+        state[lo:hi], q[lo:hi] = part, qp
+        tail, t = tail2, t2
+    b.check_append({"state": state, "tail": tail, "t": t, "len": n, "q": q})
+    whole.check_append(whole.append())
+    assert int(b.err.item()) == 0
