@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "kernels.cuh"
@@ -206,7 +207,7 @@ bool encode_weight_map(CUtensorMap* map, const void* W, int64_t N, int64_t K) {
 namespace mtla {
 mtla_status check_call_dims(const mtla_dims* d) { return check_dims(d); }
 int current_device_sms() {
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64] = {};  // (calls come from any host thread)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < 64 && cached[dev] > 0) return cached[dev];

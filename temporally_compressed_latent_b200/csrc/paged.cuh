@@ -2,6 +2,8 @@
 // search, and the work partition of the attention kernels.
 #pragma once
 
+#include <atomic>
+
 #include "kernels.cuh"
 
 namespace mtla {

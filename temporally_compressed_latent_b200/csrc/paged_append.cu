@@ -321,7 +321,7 @@ cudaError_t launch_paged_append_simt(PagedAppendArgs& a, int dtype, int sms, cud
   auto k = dtype == MTLA_BF16 ? pap::pick<__nv_bfloat16>(a.r) : pap::pick<float>(a.r);
   {
     // the shared-memory opt-in, once per instance and device
-    static uint64_t done_mask[6] = {};
+    static std::atomic<uint64_t> done_mask[6] = {};
     const int slot = (dtype == MTLA_BF16 ? 3 : 0) + (kpt == 8 ? 0 : (kpt == 32 ? 1 : 2));
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

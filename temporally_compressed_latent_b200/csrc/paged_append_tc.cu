@@ -616,7 +616,7 @@ __global__ void __maxnreg__(96) paged_append_tc_kernel(const __grid_constant__ P
 }  // namespace ptp
 
 cudaError_t launch_paged_append_tc(const PagedAppendArgs& a, const PagedAppendMaps& m, int sms, cudaStream_t st) {
-  static uint64_t done_mask = 0;
+  static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
 }  // namespace ptt
 
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, const PagedAttnMaps& m, int grid, cudaStream_t st) {
-  static uint64_t done_mask = 0;
+  static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -297,7 +297,7 @@ cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t st) {
   int cl = (a.V + 4095) / 4096;
   cl = cl < most ? cl : most;
   if (cl > 8) {  // past the portable size: allowed once per device
-    static uint64_t done_mask = 0;
+    static std::atomic<uint64_t> done_mask{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -190,3 +190,42 @@ def test_pieces_across_the_kernels(s, past):
     b.check_append({"state": state, "tail": tail, "t": t, "len": n, "q": q})
     whole.check_append(whole.append())
     assert int(b.err.item()) == 0
+
+
+def test_calls_from_several_host_threads():
+    """Every thread its own batch, stream and workspace; some of the calls are a kernel's first."""
+    import threading
+    kinds = [dict(new=[3, 1, 20], past=[100, 2000, 5]), dict(new=[520, 4], past=[3, 8]),
+             dict(new=[5, 2], past=[30, 700], **TINY), dict(new=[9], past=[50], H=5, r=384, d_R=64)]
+    jobs = []
+    for k, kw in enumerate(kinds * 2):
+        a = Batch(s=2, page_rows=16, seed=60 + k, **kw)
+        b = Batch(s=2, page_rows=16, seed=60 + k, **kw)
+        b.fill_groups()
+        jobs.append((a, b))
+    torch.cuda.synchronize()
+    out, failed = {}, []
+    gate = threading.Barrier(len(jobs))
+
+    def work(k):
+        try:
+            a, b = jobs[k]
+            st = torch.cuda.Stream()
+            gate.wait(timeout=60)
+            with torch.cuda.stream(st):
+                for _ in range(8):
+                    out[k] = a.append(), b.attn()
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001 (handed to the test)
+            failed.append((k, e))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for k, (a, b) in enumerate(jobs):
+        a.check_append(out[k][0])
+        b.check_attn(out[k][1])
+        assert int(a.err.item()) == 0 and int(b.err.item()) == 0
