@@ -162,7 +162,7 @@ __device__ __forceinline__ float2 rope_cos_sin(uint32_t pos, uint64_t turns) {
 // / s): nested divisions fold into one,
 //   kt = floor((t + 7 s - 1 + 8 s (g + q - 1)) / (8 q s)),
 // linear in t, so the sum over a sequence's items is a sum of floors of a
-// linear function, which has a logarithmic-time form (floor_sum).
+// linear function, which has a closed form (floor_sum).
 // ----------------------------------------------------------------------------
 struct PlanArgs {
   int s, tpt, q, item_cost;
@@ -170,27 +170,37 @@ struct PlanArgs {
   int one_block;   // most weight that one block takes alone
   FastDiv div_s;
 };
-// sum over i in [0, n) of floor((a i + b) / m), by the Euclidean recursion
-__device__ inline int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
-  uint64_t ans = 0;
-  while (n > 0) {
-    if (a >= m) {
-      ans += (n - 1) * n / 2 * (a / m);
-      a %= m;
+// sum over i in [0, n) of floor((a i + b) / m), n > 0, 0 < a < m, a small (tpt,
+// of at most 16, against m = 8 q s).  With b = m B + c, 0 <= c < m, it is n B and
+// the sum of floor((a i + c) / m), whose terms rise from 0 to some K by at most
+// one a step: counted by levels, level k (1 <= k <= K) holds the i from
+// ceil((m k - c) / a) on, n of them less that.  With m = a M + f and c = a C + d a
+// level's ceiling is M k - C + g_k, g_k = ceil((f k - d) / a), and g_(k + a) = g_k +
+// f: one walk over a of them gives the sum of all K.  T holds m, b and a n.
+template <typename T>
+__device__ __forceinline__ int64_t floor_sum_in(T n, T m, T a, T b) {
+  const T B = b / m, c = b - B * m, K = (a * (n - 1) + c) / m;
+  const T M = m / a, C = c / a, rounds = K / a;
+  const int f = (int)(m - M * a), d = (int)(c - C * a), rest = (int)(K - rounds * a);
+  int w = -d, g = 0, all = 0, some = 0;  // w = f k - d - a g, in (-a, 0]
+  for (int k = 1; k <= (int)a; ++k) {
+    w += f;
+    if (w > 0) {
+      w -= (int)a;
+      ++g;
     }
-    if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
-    }
-    const uint64_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const uint64_t x = m;
-    m = a;
-    a = x;
+    all += g;
+    if (k <= rest) some += g;
   }
-  return (int64_t)ans;
+  const uint64_t K_ = K, r = rounds;
+  const uint64_t ceils = M * (K_ * (K_ + 1) / 2) - C * K_ + (a * f) * (r * (r - 1) / 2) + r * (uint64_t)all +
+                         (uint64_t)(rest * f) * r + (uint64_t)some;
+  return (int64_t)((uint64_t)n * (B + K_) - ceils);
+}
+__device__ inline int64_t floor_sum(uint64_t n, uint64_t m, uint32_t a, uint64_t b) {
+  // (a 64-bit division takes several times as long as a 32-bit one)
+  if ((b + m + a * n) >> 32 == 0) return floor_sum_in<uint32_t>((uint32_t)n, (uint32_t)m, a, (uint32_t)b);
+  return floor_sum_in<uint64_t>(n, m, a, b);
 }
 // cache rows below the query of time t: R = ceil(t / s) - 1 (1 <= t < 2^32)
 __device__ __forceinline__ int rows_below(const PlanArgs& a, int64_t t) { return (int)div32((uint32_t)(t - 1), a.div_s); }
@@ -216,7 +226,7 @@ static __device__ __noinline__ int64_t items_weight_many(int s, int tpt, int q, 
     return w;
   }
   const int64_t full = n / a.tpt, k = m < full ? m : full;
-  w += floor_sum((uint64_t)k, 8ull * a.q * a.s, (uint64_t)a.tpt,
+  w += floor_sum((uint64_t)k, 8ull * a.q * a.s, (uint32_t)a.tpt,
                  (uint64_t)(t0 + a.tpt + 7ll * a.s - 1 + 8ll * a.s * (((a.tpt + 7) >> 3) + a.q - 1)));
   if (m > full) w += item_tiles(a, t0 + n, n - (int)full * a.tpt);
   return w;
