@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
                               __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
           }
         }
-        if (hidden)
+        if (__builtin_expect(hidden, false))
           restore_nan<__nv_bfloat16>(a, it.b, it.row0, it.t, qe * 32, live < qe * 32 + 32 ? live : qe * 32 + 32,
                                      dst - (int64_t)i * R, true);
         continue;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
           }
         }
       }
-      if (hidden)
+      if (__builtin_expect(hidden, false))
         restore_nan<__nv_bfloat16>(a, it.b, it.row0, it.t, qe * 32, live < qe * 32 + 32 ? live : qe * 32 + 32,
                                    base - (int64_t)qe * 32 * R, false);
     }
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
             // columns of the item that this row does not see
             const uint32_t not_mine =
                 on ? (low_bits(it.R - c0) | (low_bits(R8 + it.ntok - c0) & ~low_bits(R8 - c0))) & ~vis : 0u;
-            if (__any_sync(0xffffffffu, not_mine != 0u) && __any_sync(0xffffffffu, not_finite(x))) {
+            if (__any_sync(0xffffffffu, not_mine != 0u) && __builtin_expect(__any_sync(0xffffffffu, not_finite(x)), 0)) {
               // some score is not finite: of a column that its row does not see?
               float z = 0.f;
 #pragma unroll
