@@ -127,3 +127,92 @@ def test_generic_append_over_many_rounds(dims, N, s):
     new = [N - 700, 1, 333, 2, 364]
     past = [5, 0, s, 3 * s - 1, 1000]
     Dense(new, past, s, seed=N + s, **dims).check()
+
+
+def _hold(b, c):
+    """Puts the contents of batch c (no larger, as many tokens and sequences) where b's captured calls look."""
+    b.t_prev.copy_(c.t_prev)
+    b.tok_start.copy_(c.tok_start)
+    b.d_table.fill_(-7)
+    b.d_table[:, : c.table_pages].copy_(c.d_table)
+    b.d_pages.fill_(float("nan"))
+    b.d_pages[: c.num_pages].copy_(c.d_pages)
+    for k, x in c.d.items():
+        b.d[k][: x.shape[0]].copy_(x)
+    b.err.zero_()
+
+
+@pytest.mark.parametrize("dims", [{}, TINY], ids=["main", "tiny"])
+def test_replays_follow_new_contents(dims):
+    """Attention of two batches in two graphs that share a workspace, and their appends in graphs of their own: replayed
+    after lengths, starts, tables, pages and inputs have changed, every result is that of the new contents."""
+    N, kw = 24, dict(s=2, page_rows=16, **dims)
+    large = [Batch([3, 1, 20], [1990, 2000, 1995], seed=70 + k, J_extra=8, **kw) for k in range(2)]
+    size = mtla.mtla_paged_workspace_bytes(large[0].md, 3, N, mtla.PAGED_ATTN)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    for b in large:
+        b.fill_groups()
+        b.attn(ws=ws)
+        b.append()
+    torch.cuda.synchronize()
+    graphs = {}
+    with torch.cuda.stream(st):
+        for k, b in enumerate(large):
+            for call in ("attn", "append"):
+                gr = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(gr, stream=st):
+                    o = b.attn(ws=ws) if call == "attn" else b.append()
+                graphs[call, k] = gr, o
+    st.synchronize()
+    shapes = [([10, 0, 14], [900, 31, 1500]), ([1, 22, 1], [2000, 3, 0]), ([8, 8, 8], [0, 1, 1001]), ([24, 0, 0], [77, 0, 9])]
+    for i, (new, past) in enumerate(shapes):
+        for call in ("attn", "append"):
+            held = []
+            for k, b in enumerate(large):
+                # the second graph's contents are another shape's
+                n, p = shapes[(i + k) % len(shapes)]
+                c = Batch(n, p, seed=80 + 2 * i + k, **kw)
+                if call == "attn":
+                    c.fill_groups()
+                _hold(b, c)
+                held.append(c)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(st):
+                for k in (0, 1, 0, 1):
+                    graphs[call, k][0].replay()
+            st.synchronize()
+            for k, (b, c) in enumerate(zip(large, held)):
+                o = graphs[call, k][1]
+                if call == "append":
+                    c.d_pages.copy_(b.d_pages[: c.num_pages])
+                    c.check_append(o)
+                else:
+                    c.check_attn(o)
+                assert int(b.err.item()) == 0
+
+
+def test_verification_replays_follow_new_contents():
+    rng = np.random.default_rng(5)
+    B, N, V = 4, 13, 9001
+    dev = lambda v, t: torch.tensor(np.asarray(v), dtype=t, device="cuda")
+    p, q = torch.zeros(N, V, device="cuda"), torch.zeros(N, V, device="cuda")
+    tokens, start = dev([0] * N, torch.int32), dev([0, 3, 3, 12, 13], torch.int32)
+    ua, us = torch.zeros(N, device="cuda"), torch.zeros(B, device="cuda")
+    keep, nxt, err = (dev([-9] * n, torch.int32) for n in (B, B, 1))
+    call = lambda: mtla.mtla_verify_drafts(B, N, V, p, V, q, V, tokens, start, ua, us, keep, nxt, err)
+    call()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call()
+    for lens in ([3, 0, 9, 1], [13, 0, 0, 0], [1, 1, 1, 1], [4, 4, 4, 1]):
+        z = 2 * rng.standard_normal((N, V))
+        soft = lambda a: (np.exp(a) / np.exp(a).sum(1, keepdims=True)).astype(np.float32)
+        P, Q = soft(z), soft(z + 0.4 * rng.standard_normal((N, V)))
+        tok = [int(rng.integers(0, V))] + [int(rng.choice(V, p=Q[i].astype(np.float64) / Q[i].astype(np.float64).sum())) for i in range(N - 1)]
+        s, a, u = np.concatenate([[0], np.cumsum(lens)]), rng.random(N).astype(np.float32), rng.random(B).astype(np.float32)
+        for dst, src in ((p, P), (q, Q), (tokens, tok), (start, s), (ua, a), (us, u), (err, [0])):
+            dst.copy_(torch.from_numpy(np.asarray(src)))
+        gr.replay()
+        torch.cuda.synchronize()
+        assert (keep.tolist(), nxt.tolist()) == verify_ref(P, Q, tok, s, a, u) and int(err.item()) == 0
