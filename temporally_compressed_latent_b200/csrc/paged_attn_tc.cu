@@ -42,10 +42,10 @@
 //    operand.  A score warp and a value warp issue them; eight softmax warps,
 //    two a lane quarter, rescale O only when a row's maximum grows by more
 //    than 2^8; four epilogue warps store an item while the next one starts.
-//  Measured (s = 2, H = 8): 32 single tokens over 2048 rows 20.2 us (1.88 TB/s;
+//  Measured (s = 2, H = 8): 32 single tokens over 2048 rows 20.4 us (1.86 TB/s;
 //  seven tiles a block between fixed 13 us), 128 sequences of up to 5 tokens over
-//  2048 .. 4096 rows 55.8 us (4.05 TB/s), four chunks of 1024 tokens after 16384
-//  283 us (1064 TFLOP/s).
+//  2048 .. 4096 rows 55.5 us (4.06 TB/s; 62 to 67 at the power cap), four chunks of
+//  1024 tokens after 16384 281 to 291 us (1033 to 1070 TFLOP/s).
 #include "paged.cuh"
 
 namespace mtla {

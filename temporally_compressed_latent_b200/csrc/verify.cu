@@ -19,9 +19,9 @@
 // once in a hundred draws.  They are trees of depth three in a lane and five
 // across it (an addition in double takes tens of cycles: chains of 32 made one
 // sequence's call 17 us instead of 5).
-// Bound by the two rows' HBM reads (large batches: 96 rows of 131072 take 21.0 us,
+// Bound by the two rows' HBM reads (large batches: 96 rows of 131072 take 20.6 us,
 // 4.8 TB/s) or by the chain of four dependent reads and the cluster's barriers
-// (small ones: one row of 32000 5.3 us).
+// (small ones: one row of 32000 5.2 us).
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
